@@ -1,11 +1,13 @@
-"""Build libqstate.so in-tree with nvcc for sm_100a.
+"""Build libqstate.so and libqmixer.so in-tree with nvcc for sm_100a.
 
     python -m bit_recurrent_state_decode_b200.build [--force] [-v]
 
-Each .cu unit is compiled in parallel, then linked into a shared library with
-a static CUDA runtime.  No fast-math: the step's arithmetic is specified to
-the bit (see include/qstate.h), so FMA contraction is disabled and every
-fused multiply-add in the kernels is written explicitly.
+libqstate.so (csrc/) is the quantized recurrent-state step, libqmixer.so
+(csrc/mixer/) the operators around it.  Each .cu unit is compiled in parallel,
+then each library is linked with a static CUDA runtime; a library whose
+sources are older than it is left alone.  No fast-math: the step's arithmetic
+is specified to the bit (see include/qstate.h), so FMA contraction is disabled
+and every fused multiply-add in the kernels is written explicitly.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqstate.so")
+MIXER_LIB = os.path.join(PKG, "libqmixer.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -27,24 +30,32 @@ CFLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", 
                  "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 
 
-def _deps():
-    return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "qstate.h"),
-                                                      __file__])
+# library -> folder of its units, public headers
+LIBS = {LIB: (CSRC, ("qstate.h",)), MIXER_LIB: (os.path.join(CSRC, "mixer"), ("qstate.h", "qmixer.h"))}
+
+
+def _deps(lib):
+    src, headers = LIBS[lib]
+    return ([f for ext in ("*.cu", "*.cuh", "*.h") for f in glob.glob(os.path.join(src, ext))]
+            + [os.path.join(ROOT, "include", h) for h in headers] + [__file__])
+
+
+def _lib_up_to_date(lib) -> bool:
+    if not os.path.exists(lib):
+        return False
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(d) <= t for d in _deps(lib))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return all(_lib_up_to_date(lib) for lib in LIBS)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    stale = [lib for lib in LIBS if force or not _lib_up_to_date(lib)]
+    if not stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = ["-Xptxas", "-v"] if verbose else []
 
     def compile_one(src):
@@ -56,17 +67,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
-        results = list(ex.map(compile_one, srcs))
-    if verbose:
-        for _, err in results:
-            sys.stderr.write(err)
-    objs = [o for o, _ in results]
-    tmp = LIB + ".tmp"
-    cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
+        units = {lib: sorted(glob.glob(os.path.join(LIBS[lib][0], "*.cu"))) for lib in stale}
+        results = {lib: [ex.submit(compile_one, src) for src in srcs] for lib, srcs in units.items()}
+        for lib in stale:
+            done = [r.result() for r in results[lib]]
+            if verbose:
+                for _, err in done:
+                    sys.stderr.write(err)
+            tmp = lib + ".tmp"
+            cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + [o for o, _ in done]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr}")
+            os.replace(tmp, lib)
     return LIB
 
 

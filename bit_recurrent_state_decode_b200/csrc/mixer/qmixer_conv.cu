@@ -1,0 +1,283 @@
+// qmixer_conv.cu -- the short causal convolution over the channels of a layer,
+// z_t = bias + sum_k w_k x_{t-W+1+k}, y = silu(z), for prompts and for single
+// tokens.
+//
+// Bound: memory (each x read once, each y written once; 2 W + 4 operations an
+// element).  A thread owns 16 bytes of channels (eight bf16, four binary32) and
+// walks down kWalk tokens with the last W - 1 rows in registers, so a row is
+// read once per walk; the W - 1 rows in front of a walk are read again, mostly
+// from L2.  Neighbouring threads hold neighbouring channels: every warp's load
+// is one contiguous run of 512 bytes.
+//
+// State.  Sequence s continues from state[s] and leaves its last W - 1 rows
+// there, in place.  One thread does both for its channels: the walk in which a
+// sequence starts.  It also computes the sequence's first W - 1 tokens where
+// they reach past its end, since no other thread may read a history that this
+// one overwrites.
+#include "qmixer_common.cuh"
+
+namespace qm {
+
+constexpr int kWalk = 16;
+
+struct ConvParams {
+    const void* x;
+    int64_t xs;
+    const void* w;
+    const void* bias;
+    void* state;
+    void* y;
+    int64_t ys;
+    Sequences seq;
+    int channels, vecs;
+    int64_t walks;
+    bool initial, act;
+};
+
+// V channels: V * sizeof(T) = 16 bytes, or V = 1 for any alignment.
+template <class T, int V> struct Vec {
+    float v[V];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (V == 1) v[0] = to_f32<T>(*p);
+        else if constexpr (V == 8) load8(p, v);
+        else {
+            const float4 a = *reinterpret_cast<const float4*>(p);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (V == 1) *p = from_f32<T>(v[0]);
+        else if constexpr (V == 8) store8(p, v);
+        else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < V; i++) v[i] = 0.0f;
+    }
+};
+
+template <class T, int V, int W> struct Taps {
+    float w[W][V], b[V];
+    __device__ __forceinline__ void load(const ConvParams& p, int c0) {
+        const T* wt = static_cast<const T*>(p.w) + (int64_t)c0 * W;
+        const T* bt = static_cast<const T*>(p.bias);
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+#pragma unroll
+            for (int k = 0; k < W; k++) w[k][i] = to_f32<T>(wt[i * W + k]);
+            b[i] = bt ? to_f32<T>(bt[c0 + i]) : 0.0f;
+        }
+    }
+    // rows h[0 .. W-2], then x
+    __device__ __forceinline__ Vec<T, V> apply(const Vec<T, V> (&h)[W - 1], const Vec<T, V>& x, bool act) const {
+        Vec<T, V> o;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            float z = b[i];
+#pragma unroll
+            for (int k = 0; k < W - 1; k++) z = fmaf(w[k][i], h[k].v[i], z);
+            z = fmaf(w[W - 1][i], x.v[i], z);
+            o.v[i] = act ? silu<T>(z) : z;
+        }
+        return o;
+    }
+};
+
+template <class T, int V, int W>
+__global__ void __launch_bounds__(128) conv_kernel(const ConvParams p) {
+    const int64_t id = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    const int64_t walk = id / p.vecs;
+    const int c0 = int(id % p.vecs) * V;
+    T* const st = static_cast<T*>(p.state);
+    if (walk >= p.walks) {
+        // one thread per sequence and channels: an empty sequence that starts
+        // from zeros leaves zeros (no walk holds a token of it)
+        const int64_t s = walk - p.walks;
+        if (s < p.seq.n && st && !p.initial && p.seq.start((int)s + 1) <= p.seq.start((int)s)) {
+            Vec<T, V> z;
+            z.zero();
+#pragma unroll
+            for (int r = 0; r < W - 1; r++) z.store(st + (s * (W - 1) + r) * (int64_t)p.channels + c0);
+        }
+        return;
+    }
+    const T* const x = static_cast<const T*>(p.x) + c0;
+    T* const y = static_cast<T*>(p.y) + c0;
+    Taps<T, V, W> taps;
+    taps.load(p, c0);
+
+    const int64_t stop = p.seq.start(p.seq.n);
+    const int64_t t0 = walk * kWalk;
+    int64_t t1 = t0 + kWalk < stop ? t0 + kWalk : stop;
+    if (t0 >= t1) return;
+    int s = sequence_at(p.seq, t0);
+    int64_t t = t0, from = p.seq.start(s), to = p.seq.start(s + 1);
+    if (t < from) t = from;              // tokens in front of the first sequence
+    Vec<T, V> h[W - 1];
+    if (t > from && t < to) {
+        // inside a sequence: its first W - 1 tokens belong to the walk it starts in
+        if (t - from < W - 1) t = from + W - 1 < to ? from + W - 1 : to;
+#pragma unroll
+        for (int r = 0; r < W - 1; r++) {
+            const int64_t at = t - (W - 1) + r;
+            if (t < t1 && at >= from) h[r].load(x + at * p.xs);
+            else h[r].zero();
+        }
+    }
+    while (t < t1) {
+        while (t >= to && s + 1 < p.seq.n) {        // the next sequence that holds a token
+            s++;
+            from = p.seq.start(s);
+            to = p.seq.start(s + 1);
+            if (t < from) t = from;
+        }
+        if (t >= to || t >= t1) return;
+        int64_t end = to < t1 ? to : t1;
+        if (t == from) {
+            T* const own = st ? st + (int64_t)s * (W - 1) * p.channels + c0 : nullptr;
+#pragma unroll
+            for (int r = 0; r < W - 1; r++) {
+                if (p.initial) h[r].load(own + (int64_t)r * p.channels);
+                else h[r].zero();
+            }
+            if (own) {
+                Vec<T, V> last[W - 1];
+#pragma unroll
+                for (int r = 0; r < W - 1; r++) {
+                    const int64_t at = to - (W - 1) + r;
+                    if (at >= from) last[r].load(x + at * p.xs);
+                    else {
+                        last[r].zero();
+#pragma unroll
+                        for (int q = 0; q < W - 1; q++)     // row at - from of the history, from its end
+                            if (at - from + (W - 1) == q) last[r] = h[q];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < W - 1; r++) last[r].store(own + (int64_t)r * p.channels);
+            }
+            // its first W - 1 tokens, also past the end of this walk
+            const int64_t least = from + W - 1 < to ? from + W - 1 : to;
+            if (end < least) end = least;
+        }
+        // four rows in flight
+        for (; t + 4 <= end; t += 4) {
+            Vec<T, V> r[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) r[i].load(x + (t + i) * p.xs);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                taps.apply(h, r[i], p.act).store(y + (t + i) * p.ys);
+#pragma unroll
+                for (int k = 0; k + 1 < W - 1; k++) h[k] = h[k + 1];
+                h[W - 2] = r[i];
+            }
+        }
+        for (; t < end; t++) {
+            Vec<T, V> r;
+            r.load(x + t * p.xs);
+            taps.apply(h, r, p.act).store(y + t * p.ys);
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; k++) h[k] = h[k + 1];
+            h[W - 2] = r;
+        }
+    }
+}
+
+// One token of each sequence: the state moves on by one row.
+template <class T, int V, int W>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
+    const int64_t id = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    const int64_t b = id / p.vecs;
+    if (b >= p.seq.n) return;
+    const int c0 = int(id % p.vecs) * V;
+    T* const st = static_cast<T*>(p.state) + b * (W - 1) * p.channels + c0;
+    Vec<T, V> h[W - 1], x;
+#pragma unroll
+    for (int r = 0; r < W - 1; r++) h[r].load(st + (int64_t)r * p.channels);
+    x.load(static_cast<const T*>(p.x) + b * p.xs + c0);
+    Taps<T, V, W> taps;
+    taps.load(p, c0);
+    taps.apply(h, x, p.act).store(static_cast<T*>(p.y) + b * p.ys + c0);
+#pragma unroll
+    for (int r = 0; r + 1 < W - 1; r++) h[r + 1].store(st + (int64_t)r * p.channels);
+    x.store(st + (int64_t)(W - 2) * p.channels);
+}
+
+template <class T, int V, int W> void launch(const ConvParams& p, bool step, cudaStream_t st) {
+    const int64_t threads = (step ? (int64_t)p.seq.n : p.walks + (p.state && !p.initial ? p.seq.n : 0)) * p.vecs;
+    const int64_t blocks = (threads + 127) / 128;
+    if (!blocks) return;
+    if (step) conv_step_kernel<T, V, W><<<(unsigned)blocks, 128, 0, st>>>(p);
+    else conv_kernel<T, V, W><<<(unsigned)blocks, 128, 0, st>>>(p);
+}
+
+template <class T, int V> void launch_w(const ConvParams& p, int width, bool step, cudaStream_t st) {
+    if (width == 2) launch<T, V, 2>(p, step, st);
+    else if (width == 3) launch<T, V, 3>(p, step, st);
+    else launch<T, V, 4>(p, step, st);
+}
+
+int conv_any(ConvParams& p, int width, int dtype, bool step, cudaStream_t st) {
+    const int wide = dtype == QSTATE_BF16 ? 8 : 4;
+    // 16-byte accesses need the channels, both strides and all bases to allow
+    // them; else element by element
+    const bool vec = p.channels % wide == 0 && p.xs % wide == 0 && p.ys % wide == 0 && aligned(p.x, 16) &&
+                     aligned(p.y, 16) && aligned(p.state, 16);
+    p.vecs = vec ? p.channels / wide : p.channels;
+    p.walks = (p.seq.tokens + kWalk - 1) / kWalk;
+    if (((p.walks + p.seq.n) * p.vecs + 127) / 128 > INT32_MAX) return QSTATE_EUNSUPPORTED;
+    if (dtype == QSTATE_BF16) {
+        if (vec) launch_w<bf16, 8>(p, width, step, st);
+        else launch_w<bf16, 1>(p, width, step, st);
+    } else {
+        if (vec) launch_w<float, 4>(p, width, step, st);
+        else launch_w<float, 1>(p, width, step, st);
+    }
+    return launched();
+}
+
+}  // namespace qm
+
+extern "C" {
+
+int qmixer_conv(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state, void* y,
+                int64_t y_stride, const int32_t* seq_starts, int32_t sequences, int64_t tokens,
+                int32_t channels, int32_t width, int32_t dtype, int32_t flags, qstate_stream stream) {
+    if (!qm::known(dtype) || sequences < 0 || tokens < 0 || tokens > INT32_MAX || channels < 1 || width < 1)
+        return QSTATE_EINVAL;
+    if (flags & ~(QMIXER_INITIAL | QMIXER_SILU)) return QSTATE_EINVAL;
+    if (x_stride < channels || y_stride < channels) return QSTATE_EINVAL;
+    if (!seq_starts && sequences && tokens % sequences) return QSTATE_EINVAL;
+    if ((flags & QMIXER_INITIAL) && !state && sequences) return QSTATE_EINVAL;
+    const int size = qm::size_of(dtype);
+    if (!qm::aligned(x, size) || !qm::aligned(y, size) || !qm::aligned(weight, size) || !qm::aligned(bias, size) ||
+        !qm::aligned(state, size) || !qm::aligned(seq_starts, 4))
+        return QSTATE_EINVAL;
+    if (width < 2 || width > 4) return QSTATE_EUNSUPPORTED;
+    if (!sequences || (!tokens && !state)) return QSTATE_OK;
+    if (!weight || (tokens && (!x || !y))) return QSTATE_EINVAL;
+    qm::ConvParams p{x, x_stride, weight, bias, state, y, y_stride,
+                     {seq_starts, sequences, tokens, tokens / sequences}, channels, 0, 0,
+                     (flags & QMIXER_INITIAL) != 0, (flags & QMIXER_SILU) != 0};
+    return qm::conv_any(p, width, dtype, false, (cudaStream_t)stream);
+}
+
+int qmixer_conv_step(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state,
+                     void* y, int64_t y_stride, int32_t batch, int32_t channels, int32_t width, int32_t dtype,
+                     int32_t flags, qstate_stream stream) {
+    if (!qm::known(dtype) || batch < 0 || channels < 1 || width < 1 || (flags & ~QMIXER_SILU)) return QSTATE_EINVAL;
+    if (x_stride < channels || y_stride < channels) return QSTATE_EINVAL;
+    const int size = qm::size_of(dtype);
+    if (!qm::aligned(x, size) || !qm::aligned(y, size) || !qm::aligned(weight, size) || !qm::aligned(bias, size) ||
+        !qm::aligned(state, size))
+        return QSTATE_EINVAL;
+    if (width < 2 || width > 4) return QSTATE_EUNSUPPORTED;
+    if (!batch) return QSTATE_OK;
+    if (!x || !y || !weight || !state) return QSTATE_EINVAL;
+    qm::ConvParams p{x, x_stride, weight, bias, state, y, y_stride, {nullptr, batch, batch, 1}, channels, 0, 0,
+                     false, (flags & QMIXER_SILU) != 0};
+    return qm::conv_any(p, width, dtype, true, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,263 @@
+// qmixer_norm.cu -- root-mean-square norm of a row, y = h / sqrt(mean(h^2) +
+// eps) * weight, with h = x + residual or x silu(gate) formed on the way in and
+// y rounded once on the way out: to the inputs' type, or to 8-bit codes with a
+// binary32 scale per row or per group of columns.
+//
+// Bound: memory (x and the second operand read once, y written once).  kThreads
+// threads hold one row in registers between the sum of squares and the output,
+// so nothing is read twice; each thread takes eight consecutive columns at a
+// time, kThreads * 8 columns apart, all loads of a row in flight together.  The
+// groups of the 8-bit scales are powers of two of at most 256 columns: 32 lanes
+// or fewer of one warp, joined by shuffles.
+#include "qmixer_common.cuh"
+
+namespace qm {
+
+struct NormParams {
+    const void* x;
+    int64_t xs;
+    void* other;
+    int64_t os;
+    const void* w;
+    void* y;
+    int64_t ys;
+    float* scales;
+    int64_t rows;
+    int columns, group;
+    float eps;
+    int before, out;
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void row8(const T* p, int left, float (&v)[8]) {
+    if constexpr (VEC) {
+        load8(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = i < left ? to_f32<T>(p[i]) : 0.0f;
+    }
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ void put8(T* p, int left, const float (&v)[8]) {
+    if constexpr (VEC) {
+        store8(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < left) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The scale of a group from its largest magnitude (as bits: an integer maximum
+// keeps a NaN) and the codes of eight of its values.
+struct Codes {
+    float scale, inv;
+    bool tiny;
+    __device__ __forceinline__ Codes(uint32_t most, float qmax) {
+        const bool bad = most >= 0x7f800000u;
+        scale = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(most), qmax);
+        inv = bad || scale == 0.0f ? 0.0f : __frcp_rn(scale);
+        tiny = scale < 1e-36f && scale > 0.0f;       // its reciprocal may overflow
+        if (tiny) inv = 0.0f;
+        if (bad) inv = __uint_as_float(0x7fc00000u);
+    }
+    __device__ __forceinline__ float at(float y) const {
+        return tiny ? __fdiv_rn(y, scale) : inv != inv ? 0.0f : y * inv;
+    }
+    __device__ __forceinline__ uint2 int8(const float (&y)[8]) const {
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float q = fminf(fmaxf(at(y[i]), -127.0f), 127.0f);
+            c[i] = __float_as_uint(q + 12582912.0f) & 0xffu;      // 1.5 * 2^23: rounds half to even
+        }
+        return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+    }
+    __device__ __forceinline__ uint2 e4m3(const float (&y)[8]) const {
+        return make_uint2(e4m3x2(at(y[0]), at(y[1])) | e4m3x2(at(y[2]), at(y[3])) << 16,
+                          e4m3x2(at(y[4]), at(y[5])) | e4m3x2(at(y[6]), at(y[7])) << 16);
+    }
+};
+
+template <class T, bool VEC, int THREADS, int N>
+__global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(const NormParams p) {
+    constexpr int kBlock = THREADS < 128 ? 128 : THREADS;
+    constexpr int kWarps = THREADS / 32;
+    __shared__ float sums[kWarps];
+    __shared__ uint32_t tops[kWarps];
+    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t row = THREADS == 32 ? blockIdx.x * (int64_t)(kBlock / 32) + threadIdx.x / 32 : blockIdx.x;
+    if (row >= p.rows) return;                   // THREADS > 32: one row per block, never taken
+    const T* const x = static_cast<const T*>(p.x) + row * p.xs;
+    T* const other = static_cast<T*>(p.other) + row * p.os;
+    const T* const w = static_cast<const T*>(p.w);
+
+    float h[N][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+        if (left > 0) row8<T, VEC>(x + c, left, h[i]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; j++) h[i][j] = 0.0f;
+    }
+    if (p.before != QMIXER_BEFORE_NONE) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+            if (left <= 0) continue;
+            float o[8];
+            row8<T, VEC>(other + c, left, o);
+            if (p.before == QMIXER_BEFORE_RESIDUAL) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) h[i][j] += o[j];
+                put8<T, VEC>(other + c, left, h[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) h[i][j] *= silu<T>(o[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) sum = fmaf(h[i][j], h[i][j], sum);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    if constexpr (THREADS > 32) {
+        if ((tid & 31) == 0) sums[tid / 32] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; i++) sum += sums[i];
+    }
+    const float r = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, (float)p.columns) + p.eps));
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+        if (left <= 0) continue;
+        float g[8];
+        row8<T, VEC>(w + c, left, g);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            h[i][j] = h[i][j] * r * g[j];
+            if (VEC || j < left) most = max(most, __float_as_uint(h[i][j]) & 0x7fffffffu);
+        }
+    }
+    if (p.out == QMIXER_OUT_SAME) {
+        T* const y = static_cast<T*>(p.y) + row * p.ys;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+            if (left > 0) put8<T, VEC>(y + c, left, h[i]);
+        }
+        return;
+    }
+    uint8_t* const y = static_cast<uint8_t*>(p.y) + row * p.ys;
+    const float qmax = p.out == QMIXER_OUT_INT8 ? 127.0f : 448.0f;
+    if (!p.group) {
+        most = __reduce_max_sync(~0u, most);
+        if constexpr (THREADS > 32) {
+            if ((tid & 31) == 0) tops[tid / 32] = most;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kWarps; i++) most = max(most, tops[i]);
+        }
+    }
+    const int lanes = p.group >> 3, ngroups = p.group ? p.columns / p.group : 1;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+        uint32_t m = most;
+        if (p.group) {
+            m = 0;
+            if (left > 0)
+#pragma unroll
+                for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(h[i][j]) & 0x7fffffffu);
+            for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
+        }
+        if (left <= 0) continue;
+        const Codes q(m, qmax);
+        if (p.group ? (c & (p.group - 1)) == 0 : c == 0)
+            p.scales[row * ngroups + (p.group ? c / p.group : 0)] = q.scale;
+        const uint2 b = p.out == QMIXER_OUT_INT8 ? q.int8(h[i]) : q.e4m3(h[i]);
+        if constexpr (VEC) {
+            *reinterpret_cast<uint2*>(y + c) = b;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (j < left) y[c + j] = (uint8_t)((j < 4 ? b.x : b.y) >> (j % 4 * 8));
+        }
+    }
+}
+
+template <class T, bool VEC, int THREADS, int N> void launch_norm(const NormParams& p, cudaStream_t st) {
+    constexpr int kBlock = THREADS < 128 ? 128 : THREADS;
+    const int64_t per = kBlock / THREADS;
+    norm_kernel<T, VEC, THREADS, N><<<(unsigned)((p.rows + per - 1) / per), kBlock, 0, st>>>(p);
+}
+
+// A row of up to 32 * 8 * N columns in one warp, N = 1, 2, 4, 8; wider ones, or
+// few rows, in 128 or 512 threads.
+template <class T, bool VEC> void dispatch_norm(const NormParams& p, cudaStream_t st) {
+    const int v = (p.columns + 7) / 8;
+    const bool few = p.rows < 148 * 8;
+    if (v <= 32) launch_norm<T, VEC, 32, 1>(p, st);
+    else if (!few && v <= 64) launch_norm<T, VEC, 32, 2>(p, st);
+    else if (!few && v <= 128) launch_norm<T, VEC, 32, 4>(p, st);
+    else if (!few && v <= 256) launch_norm<T, VEC, 32, 8>(p, st);
+    else if (v <= 128) launch_norm<T, VEC, 128, 1>(p, st);
+    else if (v <= 256) launch_norm<T, VEC, 128, 2>(p, st);
+    else if (v <= 512) launch_norm<T, VEC, 128, 4>(p, st);
+    else if (v <= 1024) launch_norm<T, VEC, 512, 2>(p, st);
+    else if (v <= 2048) launch_norm<T, VEC, 512, 4>(p, st);
+    else launch_norm<T, VEC, 512, 8>(p, st);
+}
+
+}  // namespace qm
+
+extern "C" int qmixer_norm(const void* x, int64_t x_stride, void* other, int64_t other_stride,
+                           const void* weight, void* y, int64_t y_stride, float* scales, int64_t rows,
+                           int32_t columns, int32_t group, float eps, int32_t dtype, int32_t before,
+                           int32_t out, qstate_stream stream) {
+    if (!qm::known(dtype) || rows < 0 || columns < 1 || group < 0 || !(eps >= 0.0f) || eps > 3.4e38f)
+        return QSTATE_EINVAL;
+    if (before < QMIXER_BEFORE_NONE || before > QMIXER_BEFORE_GATE || out < QMIXER_OUT_SAME || out > QMIXER_OUT_E4M3)
+        return QSTATE_EINVAL;
+    if (x_stride < columns || y_stride < columns || (before && other_stride < columns)) return QSTATE_EINVAL;
+    if (group && (out == QMIXER_OUT_SAME || columns % group)) return QSTATE_EINVAL;
+    const int size = qm::size_of(dtype), ysize = out == QMIXER_OUT_SAME ? size : 1;
+    if (!qm::aligned(x, size) || !qm::aligned(other, size) || !qm::aligned(weight, size) || !qm::aligned(y, ysize) ||
+        !qm::aligned(scales, 4))
+        return QSTATE_EINVAL;
+    if (columns > 32768 || rows > INT32_MAX) return QSTATE_EUNSUPPORTED;
+    if (group && (group < 8 || group > 256 || (group & (group - 1)))) return QSTATE_EUNSUPPORTED;
+    if (!rows) return QSTATE_OK;
+    if (!x || !weight || !y || (before && !other) || (out && !scales)) return QSTATE_EINVAL;
+    const qm::NormParams p{x, x_stride, other, other_stride, weight, y, y_stride, scales,
+                           rows, columns, group, eps, before, out};
+    // eight columns at a time where columns, strides and bases allow 16-byte
+    // accesses (8-byte ones of codes); else element by element
+    const int unit = 16 / size;
+    const bool vec = columns % 8 == 0 && x_stride % unit == 0 && qm::aligned(x, 16) && qm::aligned(weight, 16) &&
+                     (!before || (other_stride % unit == 0 && qm::aligned(other, 16))) &&
+                     (out ? y_stride % 8 == 0 && qm::aligned(y, 8) : y_stride % unit == 0 && qm::aligned(y, 16));
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (dtype == QSTATE_BF16) {
+        if (vec) qm::dispatch_norm<qm::bf16, true>(p, st);
+        else qm::dispatch_norm<qm::bf16, false>(p, st);
+    } else {
+        if (vec) qm::dispatch_norm<float, true>(p, st);
+        else qm::dispatch_norm<float, false>(p, st);
+    }
+    return qm::launched();
+}

@@ -1,0 +1,220 @@
+// qmixer_quantize.cu -- binary32 states into the codes and scales of a low-bit
+// object: what stands between a prompt's scan and the first decode step.
+//
+// The arithmetic is the dynamic rule of qstate.h on a fresh state (scale =
+// cvt(max / Qmax), code = clamp(round_half_even(S * inv)), the product exact),
+// bit for bit.  Bound: memory (four bytes read, bits / 8 written an element).  A
+// CTA takes one tile and holds it in registers: a thread eight consecutive
+// columns at a time, so that one scale of a whole tile (group 0) costs no second
+// read.  Groups are joined by shuffles where they are a power of two of lanes,
+// else through shared memory.
+#include "qmixer_common.cuh"
+
+namespace qm {
+
+constexpr int kMaxMixedHeads = 512;
+
+struct QuantParams {
+    const float* S;
+    uint8_t* codes;
+    void* scales;
+    float* ref;
+    int heads, group, bits;
+    bool scale_f32, rotate, mixed;
+    int64_t row_bytes, tile_bytes;
+    uint8_t head_bits[kMaxMixedHeads];
+    uint32_t head_off[kMaxMixedHeads];
+};
+
+// x * inv rounded half to even from the exact product: the error of the rounded
+// product decides where it lies on a tie.
+__device__ __forceinline__ int code_of(float x, float inv, float qmax) {
+    const float w = __fmul_rn(x, inv);
+    if (!(fabsf(w) < qmax + 1.0f)) return (int)copysignf(qmax, w);
+    const float e = fmaf(x, inv, -w);               // exact
+    float r = rintf(w);
+    const float d = w - r;                          // exact, |d| <= 1/2
+    if (fabsf(d) == 0.5f && e != 0.0f) {
+        // w lies on a tie and the product beside it
+        const float up = r + (d > 0.0f ? 1.0f : 0.0f), down = up - 1.0f;
+        r = e > 0.0f ? up : down;
+    }
+    return (int)fminf(fmaxf(r, -qmax), qmax);
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantParams p) {
+    constexpr int kVecs = DK * DV / 8, kEach = kVecs / 256, kRow = DV / 8;
+    __shared__ uint32_t tops[kVecs];                // group maxima, or one per warp
+    const int64_t tile = blockIdx.x;
+    const int h = int(tile % p.heads);
+    const int64_t row = tile / p.heads;
+    const int bits = p.mixed ? p.head_bits[h] : p.bits;
+    uint8_t* const codes = p.codes + row * p.row_bytes + (p.mixed ? (int64_t)p.head_off[h] : h * p.tile_bytes);
+    const float* const S = p.S + tile * (DK * DV);
+    float v[kEach][8];
+#pragma unroll
+    for (int i = 0; i < kEach; i++) load8(S + (i * 256 + threadIdx.x) * 8, v[i]);
+    if (p.rotate) {
+        // the butterfly of qstate.h along d_v, one rounding per sum; a row is
+        // kRow neighbouring lanes of eight columns
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+#pragma unroll
+            for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (!(j & s)) {
+                        const float a = v[i][j], b = v[i][j | s];
+                        v[i][j] = a + b;
+                        v[i][j | s] = a - b;
+                    }
+            for (int s = 1; s < kRow; s <<= 1) {
+                const bool high = threadIdx.x & s;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float o = __shfl_xor_sync(~0u, v[i][j], s);
+                    v[i][j] = high ? o - v[i][j] : v[i][j] + o;
+                }
+            }
+        }
+    }
+    if (p.ref) {
+#pragma unroll
+        for (int i = 0; i < kEach; i++) store8(p.ref + tile * (DK * DV) + (i * 256 + threadIdx.x) * 8, v[i]);
+    }
+    if (bits == 32) {
+#pragma unroll
+        for (int i = 0; i < kEach; i++)
+            store8(reinterpret_cast<float*>(codes) + (i * 256 + threadIdx.x) * 8, v[i]);
+        return;
+    }
+    uint32_t m[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        m[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) m[i] = max(m[i], __float_as_uint(v[i][j]) & 0x7fffffffu);
+    }
+    const int lanes = p.group / 8;
+    if (!p.group) {
+        uint32_t all = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; i++) all = max(all, m[i]);
+        all = __reduce_max_sync(~0u, all);
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = all;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; w++) all = max(all, tops[w]);
+#pragma unroll
+        for (int i = 0; i < kEach; i++) m[i] = all;
+    } else if ((lanes & (lanes - 1)) == 0) {
+        for (int d = 1; d < lanes; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < kEach; i++) m[i] = max(m[i], __shfl_xor_sync(~0u, m[i], d));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kEach; i++) tops[i * 256 + threadIdx.x] = m[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const int u = i * 256 + threadIdx.x, first = u / kRow * kRow + u % kRow / lanes * lanes;
+            for (int j = 0; j < lanes; j++) m[i] = max(m[i], tops[first + j]);
+        }
+    }
+    const float qmax = (float)((1 << (bits - 1)) - 1);
+    const int per_row = p.group ? DV / p.group : 1;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        const int u = i * 256 + threadIdx.x, r = u / kRow, c8 = u % kRow;
+        float scale = __fdiv_rn(__uint_as_float(m[i]), qmax);
+        if (!p.scale_f32) scale = fminf(__half2float(__float2half_rn(scale)), 65504.0f);
+        const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale);
+        const bool first = p.group ? c8 % lanes == 0 : u == 0;
+        if (first) {
+            const int64_t at = p.group ? (tile * DK + r) * per_row + c8 / lanes : tile;
+            if (p.scale_f32) static_cast<float*>(p.scales)[at] = scale;
+            else static_cast<__half*>(p.scales)[at] = __float2half_rn(scale);
+        }
+        int c[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) c[j] = code_of(v[i][j], inv, qmax);
+        uint32_t lo = 0, hi = 0;
+        if (bits == 8) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                lo |= (uint32_t)(c[j] & 255) << (8 * j);
+                hi |= (uint32_t)(c[j + 4] & 255) << (8 * j);
+            }
+            *reinterpret_cast<uint2*>(codes + u * 8) = make_uint2(lo, hi);
+        } else if (bits == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) lo |= (uint32_t)(c[j] & 3) << (2 * j);
+            *reinterpret_cast<uint16_t*>(codes + u * 2) = (uint16_t)lo;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                lo |= (uint32_t)(c[j] & 15) << (4 * j);
+                hi |= (uint32_t)((c[j] >> 4) & 3) << (2 * j);
+            }
+            *reinterpret_cast<uint32_t*>(codes + u * 4) = lo;
+            if (bits == 6) *reinterpret_cast<uint16_t*>(codes + DK * DV / 2 + u * 2) = (uint16_t)hi;
+        }
+    }
+}
+
+bool width_ok(int b) { return b == 2 || b == 4 || b == 6 || b == 8; }
+
+}  // namespace qm
+
+extern "C" int qmixer_quantize(const float* S, void* codes, void* scales, float* ref, int64_t rows, int32_t heads,
+                               int32_t d_k, int32_t d_v, int32_t bits, const uint8_t* head_bits, int32_t group,
+                               int32_t scale_dtype, int32_t rotation, qstate_stream stream) {
+    if (rows < 0 || heads < 1 || d_k < 8 || d_v < 8 || d_k % 8 || d_v % 8) return QSTATE_EINVAL;
+    if (rows > INT32_MAX || rows * heads > INT32_MAX) return QSTATE_EINVAL;
+    if (group < 0 || (group && (group % 8 || d_v % group))) return QSTATE_EINVAL;
+    if (scale_dtype != QSTATE_F16 && scale_dtype != QSTATE_F32) return QSTATE_EINVAL;
+    if (rotation != 0 && rotation != 1) return QSTATE_EINVAL;
+    if (head_bits) {
+        for (int i = 0; i < heads; i++)
+            if (!qm::width_ok(head_bits[i])) return QSTATE_EINVAL;
+    } else if (!qm::width_ok(bits) && bits != 32) {
+        return QSTATE_EINVAL;
+    }
+    if (!qm::aligned(S, 16) || !qm::aligned(codes, 16) || !qm::aligned(ref, 16) || !qm::aligned(scales, 4))
+        return QSTATE_EINVAL;
+    if ((d_k != 64 && d_k != 128) || (d_v != 64 && d_v != 128)) return QSTATE_EUNSUPPORTED;
+    if (head_bits && heads > qm::kMaxMixedHeads) return QSTATE_EUNSUPPORTED;
+    if (!rows) return QSTATE_OK;
+    if (!S || !codes || ((head_bits || bits != 32) && !scales)) return QSTATE_EINVAL;
+    qm::QuantParams p{};
+    p.S = S;
+    p.codes = static_cast<uint8_t*>(codes);
+    p.scales = scales;
+    p.ref = ref;
+    p.heads = heads;
+    p.group = group;
+    p.bits = bits;
+    p.scale_f32 = scale_dtype == QSTATE_F32;
+    p.rotate = rotation == 1;
+    p.mixed = head_bits != nullptr;
+    p.tile_bytes = (int64_t)d_k * d_v * bits / 8;
+    p.row_bytes = p.tile_bytes * heads;
+    if (head_bits) {
+        uint32_t off = 0;
+        for (int i = 0; i < heads; i++) {
+            p.head_bits[i] = head_bits[i];
+            p.head_off[i] = off;
+            off += (uint32_t)(d_k * d_v * head_bits[i] / 8);
+        }
+        p.row_bytes = off;
+        p.tile_bytes = 0;
+    }
+    const unsigned tiles = (unsigned)(rows * heads);
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (d_k == 64 && d_v == 64) qm::quantize_kernel<64, 64><<<tiles, 256, 0, st>>>(p);
+    else if (d_k == 64) qm::quantize_kernel<64, 128><<<tiles, 256, 0, st>>>(p);
+    else if (d_v == 64) qm::quantize_kernel<128, 64><<<tiles, 256, 0, st>>>(p);
+    else qm::quantize_kernel<128, 128><<<tiles, 256, 0, st>>>(p);
+    return qm::launched();
+}

@@ -1,0 +1,209 @@
+// qmixer_scan_rec.cu -- the prompt scan token by token, in binary32 throughout:
+// S <- a S + (dt x) B^T, y = S^T C + D x.
+//
+// A CTA takes 64 value columns of one head over one segment, with the state in
+// registers: a thread holds 8 rows x 4 columns as pairs of rows, so that B and C
+// come from shared memory as the pairs that the packed binary32 instructions take
+// (sm_100 issues two operations of a pair at once).  A token costs 48 packed
+// instructions, five 16-byte shared loads and the five shuffles that sum y over
+// the 8 or 16 threads of a column: about 75 instructions a thread, so
+// instruction issue is the bound, not memory.  kBatch tokens are staged at a
+// time while the next ones are on their way to registers.
+#include "qmixer_scan.cuh"
+
+namespace qm {
+
+
+constexpr int kBatch = kBatchTokens;
+
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+template <int N> struct RecSmem {
+    float k[2][kBatch][N], q[2][kBatch][N], x[2][kBatch][64], y[2][kBatch][64];
+    float2 ad[2][kBatch];        // decay, time step
+};
+
+template <class T, int N, bool OUT>
+__global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
+    constexpr int kThreads = N * 2, kL = N / 8;      // threads of one column group
+    extern __shared__ __align__(16) unsigned char raw[];
+    RecSmem<N>& sm = *reinterpret_cast<RecSmem<N>*>(raw);
+    const int tid = threadIdx.x;
+    Segment seg;
+    if (!find_segment(p, blockIdx.x, seg)) return;
+    if (!OUT && seg.last) return;
+    const int parts = p.dv / 64, h = blockIdx.y / parts, c0 = blockIdx.y % parts * 64;
+    const int g = h / p.per_group, r4 = tid % kL * 4, pg = tid / kL * 4;
+    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, D = OUT && p.D ? p.D[h] : 0.0f;
+
+    // rows r4 .. r4+3 and N/2 + r4 .. : four pairs of rows, four columns
+    f2 S[4][4];
+    const float* from = nullptr;
+    if (OUT && p.cut) from = p.seg_state + ((int64_t)blockIdx.x * p.heads + h) * N * p.dv;
+    else if (OUT && p.initial) from = p.state + ((int64_t)seg.sequence * p.heads + h) * N * p.dv;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = (i / 2) * (N / 2) + r4 + i % 2 * 2;
+        float4 lo = make_float4(0, 0, 0, 0), hi = lo;
+        if (from) {
+            lo = *reinterpret_cast<const float4*>(from + (int64_t)r * p.dv + c0 + pg);
+            hi = *reinterpret_cast<const float4*>(from + (int64_t)(r + 1) * p.dv + c0 + pg);
+        }
+        S[i][0] = pair(lo.x, hi.x);
+        S[i][1] = pair(lo.y, hi.y);
+        S[i][2] = pair(lo.z, hi.z);
+        S[i][3] = pair(lo.w, hi.w);
+    }
+
+    // staging: thread t brings eight elements of k and q (row t / (N/8)) and,
+    // below 128, of x (row t / 8); below kBatch a token's decay
+    const int kr = tid / (N / 8), kc = tid % (N / 8) * 8, xr = tid / 8, xc = tid % 8 * 8;
+    float nk[8], nq[8], nx[8], na = 1.0f, nd = 0.0f;
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) nk[j] = nq[j] = nx[j] = 0.0f;
+        na = 1.0f;
+        nd = 0.0f;
+        if (t0 + kr < seg.to) {
+            load8(static_cast<const T*>(p.B) + (t0 + kr) * p.Bs + (int64_t)g * N + kc, nk);
+            if (OUT) load8(static_cast<const T*>(p.C) + (t0 + kr) * p.Cs + (int64_t)g * N + kc, nq);
+        }
+        if (tid < 128 && t0 + xr < seg.to)
+            load8(static_cast<const T*>(p.x) + (t0 + xr) * p.xs + (int64_t)h * p.dv + c0 + xc, nx);
+        if (tid < kBatch && t0 + tid < seg.to) {
+            nd = time_step(load_dt(p.dt, (t0 + tid) * p.dts + h, p.dt_bf16), bias, p.softplus);
+            na = expf(nd * A);
+        }
+    };
+    auto stage = [&](int b) {
+        store8(&sm.k[b][kr][kc], nk);
+        if (OUT) store8(&sm.q[b][kr][kc], nq);
+        if (tid < 128) store8(&sm.x[b][xr][xc], nx);
+        if (tid < kBatch) sm.ad[b][tid] = make_float2(na, nd);
+    };
+
+    float total = 1.0f;
+    int b = 0;
+    fetch(seg.from);
+    stage(0);
+    __syncthreads();
+    for (int64_t t0 = seg.from; t0 < seg.to; t0 += kBatch, b ^= 1) {
+        fetch(t0 + kBatch);
+        const int n = seg.to - t0 < kBatch ? (int)(seg.to - t0) : kBatch;
+#pragma unroll 2
+        for (int t = 0; t < n; t++) {
+            const float2 ad = sm.ad[b][t];
+            const float4 xv = *reinterpret_cast<const float4*>(&sm.x[b][t][pg]);
+            const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&sm.k[b][t][r4]);
+            const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&sm.k[b][t][N / 2 + r4]);
+            const f2 k[4] = {k0.x, k0.y, k1.x, k1.y};
+            const f2 a = pair(ad.x, ad.x);
+            const f2 v[4] = {pair(xv.x * ad.y, xv.x * ad.y), pair(xv.y * ad.y, xv.y * ad.y),
+                             pair(xv.z * ad.y, xv.z * ad.y), pair(xv.w * ad.y, xv.w * ad.y)};
+            if (!OUT) total *= ad.x;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) S[i][j] = fma2(k[i], v[j], mul2(S[i][j], a));
+            if constexpr (OUT) {
+                const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(&sm.q[b][t][r4]);
+                const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(&sm.q[b][t][N / 2 + r4]);
+                const f2 q[4] = {q0.x, q0.y, q1.x, q1.y};
+                float o[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    f2 s = mul2(q[0], S[0][j]);
+#pragma unroll
+                    for (int i = 1; i < 4; i++) s = fma2(q[i], S[i][j], s);
+                    const float2 u = unpair(s);
+                    o[j] = u.x + u.y;
+                }
+                // sum over the column group's threads, scattering the four columns
+                const bool b0 = tid & 1, b1 = tid & 2;
+                float u0 = b0 ? o[2] : o[0], u1 = b0 ? o[3] : o[1];
+                u0 += __shfl_xor_sync(~0u, b0 ? o[0] : o[2], 1);
+                u1 += __shfl_xor_sync(~0u, b0 ? o[1] : o[3], 1);
+                float u = b1 ? u1 : u0;
+                u += __shfl_xor_sync(~0u, b1 ? u0 : u1, 2);
+#pragma unroll
+                for (int d = 4; d < kL; d <<= 1) u += __shfl_xor_sync(~0u, u, d);
+                if (tid % kL < 4) {
+                    const int c = pg + (b0 ? 2 : 0) + (b1 ? 1 : 0);
+                    sm.y[b][t][c] = fmaf(D, sm.x[b][t][c], u);
+                }
+            }
+        }
+        stage(b ^ 1);
+        __syncthreads();
+        if (OUT && tid < 128 && xr < n) {
+            float o[8];
+            load8(&sm.y[b][xr][xc], o);
+            T* const y = static_cast<T*>(p.y) + (t0 + xr) * p.ys + (int64_t)h * p.dv + c0 + xc;
+            if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
+                store8(y, o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) y[j] = from_f32<T>(o[j]);
+            }
+        }
+    }
+    float* to = nullptr;
+    if (!OUT) to = p.seg_state + ((int64_t)blockIdx.x * p.heads + h) * N * p.dv;
+    else if (seg.last && p.state) to = p.state + ((int64_t)seg.sequence * p.heads + h) * N * p.dv;
+    if (to) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = (i / 2) * (N / 2) + r4 + i % 2 * 2;
+            const float2 s0 = unpair(S[i][0]), s1 = unpair(S[i][1]), s2 = unpair(S[i][2]), s3 = unpair(S[i][3]);
+            *reinterpret_cast<float4*>(to + (int64_t)r * p.dv + c0 + pg) = make_float4(s0.x, s1.x, s2.x, s3.x);
+            *reinterpret_cast<float4*>(to + (int64_t)(r + 1) * p.dv + c0 + pg) = make_float4(s0.y, s1.y, s2.y, s3.y);
+        }
+    }
+    if (!OUT && tid == 0 && c0 == 0) p.seg_decay[(int64_t)blockIdx.x * p.heads + h] = total;
+}
+
+template <class T, int N, bool OUT>
+void launch_rec(const ScanParams& p, int64_t segments, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(reinterpret_cast<const void*>(rec_kernel<T, N, OUT>), sizeof(RecSmem<N>), done)) return;
+    const dim3 grid((unsigned)segments, (unsigned)(p.heads * (p.dv / 64)));
+    rec_kernel<T, N, OUT><<<grid, N * 2, sizeof(RecSmem<N>), st>>>(p);
+}
+
+template <class T, int N>
+void launch_rec(const ScanParams& p, int64_t segments, bool states_only, cudaStream_t st) {
+    if (states_only) launch_rec<T, N, false>(p, segments, st);
+    else launch_rec<T, N, true>(p, segments, st);
+}
+
+void launch_scan_rec(const ScanParams& p, int dtype, int dk, int64_t segments, bool states_only, cudaStream_t st) {
+    if (dtype == QSTATE_BF16) {
+        if (dk == 64) launch_rec<bf16, 64>(p, segments, states_only, st);
+        else launch_rec<bf16, 128>(p, segments, states_only, st);
+    } else {
+        if (dk == 64) launch_rec<float, 64>(p, segments, states_only, st);
+        else launch_rec<float, 128>(p, segments, states_only, st);
+    }
+}
+
+}  // namespace qm
