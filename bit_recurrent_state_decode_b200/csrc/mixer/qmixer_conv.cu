@@ -241,43 +241,43 @@ int conv_any(ConvParams& p, int width, int dtype, bool step, cudaStream_t st) {
 
 extern "C" {
 
-int qmixer_conv(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state, void* y,
-                int64_t y_stride, const int32_t* seq_starts, int32_t sequences, int64_t tokens,
-                int32_t channels, int32_t width, int32_t dtype, int32_t flags, qstate_stream stream) {
-    if (!qm::known(dtype) || sequences < 0 || tokens < 0 || tokens > INT32_MAX || channels < 1 || width < 1)
+int qmixer_conv(const qmixer_conv_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_conv_args& a = *args;
+    if (!qm::known(a.dtype) || a.sequences < 0 || a.tokens < 0 || a.tokens > INT32_MAX || a.channels < 1 || a.width < 1)
         return QSTATE_EINVAL;
-    if (flags & ~(QMIXER_INITIAL | QMIXER_SILU)) return QSTATE_EINVAL;
-    if (x_stride < channels || y_stride < channels) return QSTATE_EINVAL;
-    if (!seq_starts && sequences && tokens % sequences) return QSTATE_EINVAL;
-    if ((flags & QMIXER_INITIAL) && !state && sequences) return QSTATE_EINVAL;
-    const int size = qm::size_of(dtype);
-    if (!qm::aligned(x, size) || !qm::aligned(y, size) || !qm::aligned(weight, size) || !qm::aligned(bias, size) ||
-        !qm::aligned(state, size) || !qm::aligned(seq_starts, 4))
+    if (a.flags & ~(QMIXER_INITIAL | QMIXER_SILU)) return QSTATE_EINVAL;
+    if (a.x_stride < a.channels || a.y_stride < a.channels) return QSTATE_EINVAL;
+    if (!a.seq_starts && a.sequences && a.tokens % a.sequences) return QSTATE_EINVAL;
+    if ((a.flags & QMIXER_INITIAL) && !a.state && a.sequences) return QSTATE_EINVAL;
+    const int size = qm::size_of(a.dtype);
+    if (!qm::aligned(a.x, size) || !qm::aligned(a.y, size) || !qm::aligned(a.weight, size) || !qm::aligned(a.bias, size) ||
+        !qm::aligned(a.state, size) || !qm::aligned(a.seq_starts, 4))
         return QSTATE_EINVAL;
-    if (width < 2 || width > 4) return QSTATE_EUNSUPPORTED;
-    if (!sequences || (!tokens && !state)) return QSTATE_OK;
-    if (!weight || (tokens && (!x || !y))) return QSTATE_EINVAL;
-    qm::ConvParams p{x, x_stride, weight, bias, state, y, y_stride,
-                     {seq_starts, sequences, tokens, tokens / sequences}, channels, 0, 0,
-                     (flags & QMIXER_INITIAL) != 0, (flags & QMIXER_SILU) != 0};
-    return qm::conv_any(p, width, dtype, false, (cudaStream_t)stream);
+    if (a.width < 2 || a.width > 4) return QSTATE_EUNSUPPORTED;
+    if (!a.sequences || (!a.tokens && !a.state)) return QSTATE_OK;
+    if (!a.weight || (a.tokens && (!a.x || !a.y))) return QSTATE_EINVAL;
+    qm::ConvParams p{a.x, a.x_stride, a.weight, a.bias, a.state, a.y, a.y_stride,
+                     {a.seq_starts, a.sequences, a.tokens, a.tokens / a.sequences}, a.channels, 0, 0,
+                     (a.flags & QMIXER_INITIAL) != 0, (a.flags & QMIXER_SILU) != 0};
+    return qm::conv_any(p, a.width, a.dtype, false, (cudaStream_t)stream);
 }
 
-int qmixer_conv_step(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state,
-                     void* y, int64_t y_stride, int32_t batch, int32_t channels, int32_t width, int32_t dtype,
-                     int32_t flags, qstate_stream stream) {
-    if (!qm::known(dtype) || batch < 0 || channels < 1 || width < 1 || (flags & ~QMIXER_SILU)) return QSTATE_EINVAL;
-    if (x_stride < channels || y_stride < channels) return QSTATE_EINVAL;
-    const int size = qm::size_of(dtype);
-    if (!qm::aligned(x, size) || !qm::aligned(y, size) || !qm::aligned(weight, size) || !qm::aligned(bias, size) ||
-        !qm::aligned(state, size))
+int qmixer_conv_step(const qmixer_conv_step_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_conv_step_args& a = *args;
+    if (!qm::known(a.dtype) || a.batch < 0 || a.channels < 1 || a.width < 1 || (a.flags & ~QMIXER_SILU)) return QSTATE_EINVAL;
+    if (a.x_stride < a.channels || a.y_stride < a.channels) return QSTATE_EINVAL;
+    const int size = qm::size_of(a.dtype);
+    if (!qm::aligned(a.x, size) || !qm::aligned(a.y, size) || !qm::aligned(a.weight, size) || !qm::aligned(a.bias, size) ||
+        !qm::aligned(a.state, size))
         return QSTATE_EINVAL;
-    if (width < 2 || width > 4) return QSTATE_EUNSUPPORTED;
-    if (!batch) return QSTATE_OK;
-    if (!x || !y || !weight || !state) return QSTATE_EINVAL;
-    qm::ConvParams p{x, x_stride, weight, bias, state, y, y_stride, {nullptr, batch, batch, 1}, channels, 0, 0,
-                     false, (flags & QMIXER_SILU) != 0};
-    return qm::conv_any(p, width, dtype, true, (cudaStream_t)stream);
+    if (a.width < 2 || a.width > 4) return QSTATE_EUNSUPPORTED;
+    if (!a.batch) return QSTATE_OK;
+    if (!a.x || !a.y || !a.weight || !a.state) return QSTATE_EINVAL;
+    qm::ConvParams p{a.x, a.x_stride, a.weight, a.bias, a.state, a.y, a.y_stride, {nullptr, a.batch, a.batch, 1}, a.channels, 0, 0,
+                     false, (a.flags & QMIXER_SILU) != 0};
+    return qm::conv_any(p, a.width, a.dtype, true, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -225,34 +225,33 @@ template <class T, bool VEC> void dispatch_norm(const NormParams& p, cudaStream_
 
 }  // namespace qm
 
-extern "C" int qmixer_norm(const void* x, int64_t x_stride, void* other, int64_t other_stride,
-                           const void* weight, void* y, int64_t y_stride, float* scales, int64_t rows,
-                           int32_t columns, int32_t group, float eps, int32_t dtype, int32_t before,
-                           int32_t out, qstate_stream stream) {
-    if (!qm::known(dtype) || rows < 0 || columns < 1 || group < 0 || !(eps >= 0.0f) || eps > 3.4e38f)
+extern "C" int qmixer_norm(const qmixer_norm_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_norm_args& a = *args;
+    if (!qm::known(a.dtype) || a.rows < 0 || a.columns < 1 || a.group < 0 || !(a.eps >= 0.0f) || a.eps > 3.4e38f)
         return QSTATE_EINVAL;
-    if (before < QMIXER_BEFORE_NONE || before > QMIXER_BEFORE_GATE || out < QMIXER_OUT_SAME || out > QMIXER_OUT_E4M3)
+    if (a.before < QMIXER_BEFORE_NONE || a.before > QMIXER_BEFORE_GATE || a.out < QMIXER_OUT_SAME || a.out > QMIXER_OUT_E4M3)
         return QSTATE_EINVAL;
-    if (x_stride < columns || y_stride < columns || (before && other_stride < columns)) return QSTATE_EINVAL;
-    if (group && (out == QMIXER_OUT_SAME || columns % group)) return QSTATE_EINVAL;
-    const int size = qm::size_of(dtype), ysize = out == QMIXER_OUT_SAME ? size : 1;
-    if (!qm::aligned(x, size) || !qm::aligned(other, size) || !qm::aligned(weight, size) || !qm::aligned(y, ysize) ||
-        !qm::aligned(scales, 4))
+    if (a.x_stride < a.columns || a.y_stride < a.columns || (a.before && a.other_stride < a.columns)) return QSTATE_EINVAL;
+    if (a.group && (a.out == QMIXER_OUT_SAME || a.columns % a.group)) return QSTATE_EINVAL;
+    const int size = qm::size_of(a.dtype), ysize = a.out == QMIXER_OUT_SAME ? size : 1;
+    if (!qm::aligned(a.x, size) || !qm::aligned(a.other, size) || !qm::aligned(a.weight, size) || !qm::aligned(a.y, ysize) ||
+        !qm::aligned(a.scales, 4))
         return QSTATE_EINVAL;
-    if (columns > 32768 || rows > INT32_MAX) return QSTATE_EUNSUPPORTED;
-    if (group && (group < 8 || group > 256 || (group & (group - 1)))) return QSTATE_EUNSUPPORTED;
-    if (!rows) return QSTATE_OK;
-    if (!x || !weight || !y || (before && !other) || (out && !scales)) return QSTATE_EINVAL;
-    const qm::NormParams p{x, x_stride, other, other_stride, weight, y, y_stride, scales,
-                           rows, columns, group, eps, before, out};
-    // eight columns at a time where columns, strides and bases allow 16-byte
+    if (a.columns > 32768 || a.rows > INT32_MAX) return QSTATE_EUNSUPPORTED;
+    if (a.group && (a.group < 8 || a.group > 256 || (a.group & (a.group - 1)))) return QSTATE_EUNSUPPORTED;
+    if (!a.rows) return QSTATE_OK;
+    if (!a.x || !a.weight || !a.y || (a.before && !a.other) || (a.out && !a.scales)) return QSTATE_EINVAL;
+    const qm::NormParams p{a.x, a.x_stride, a.other, a.other_stride, a.weight, a.y, a.y_stride, a.scales,
+                           a.rows, a.columns, a.group, a.eps, a.before, a.out};
+    // eight a.columns at a time where a.columns, strides and bases allow 16-byte
     // accesses (8-byte ones of codes); else element by element
     const int unit = 16 / size;
-    const bool vec = columns % 8 == 0 && x_stride % unit == 0 && qm::aligned(x, 16) && qm::aligned(weight, 16) &&
-                     (!before || (other_stride % unit == 0 && qm::aligned(other, 16))) &&
-                     (out ? y_stride % 8 == 0 && qm::aligned(y, 8) : y_stride % unit == 0 && qm::aligned(y, 16));
+    const bool vec = a.columns % 8 == 0 && a.x_stride % unit == 0 && qm::aligned(a.x, 16) && qm::aligned(a.weight, 16) &&
+                     (!a.before || (a.other_stride % unit == 0 && qm::aligned(a.other, 16))) &&
+                     (a.out ? a.y_stride % 8 == 0 && qm::aligned(a.y, 8) : a.y_stride % unit == 0 && qm::aligned(a.y, 16));
     const cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == QSTATE_BF16) {
+    if (a.dtype == QSTATE_BF16) {
         if (vec) qm::dispatch_norm<qm::bf16, true>(p, st);
         else qm::dispatch_norm<qm::bf16, false>(p, st);
     } else {

@@ -167,54 +167,54 @@ bool width_ok(int b) { return b == 2 || b == 4 || b == 6 || b == 8; }
 
 }  // namespace qm
 
-extern "C" int qmixer_quantize(const float* S, void* codes, void* scales, float* ref, int64_t rows, int32_t heads,
-                               int32_t d_k, int32_t d_v, int32_t bits, const uint8_t* head_bits, int32_t group,
-                               int32_t scale_dtype, int32_t rotation, qstate_stream stream) {
-    if (rows < 0 || heads < 1 || d_k < 8 || d_v < 8 || d_k % 8 || d_v % 8) return QSTATE_EINVAL;
-    if (rows > INT32_MAX || rows * heads > INT32_MAX) return QSTATE_EINVAL;
-    if (group < 0 || (group && (group % 8 || d_v % group))) return QSTATE_EINVAL;
-    if (scale_dtype != QSTATE_F16 && scale_dtype != QSTATE_F32) return QSTATE_EINVAL;
-    if (rotation != 0 && rotation != 1) return QSTATE_EINVAL;
-    if (head_bits) {
-        for (int i = 0; i < heads; i++)
-            if (!qm::width_ok(head_bits[i])) return QSTATE_EINVAL;
-    } else if (!qm::width_ok(bits) && bits != 32) {
+extern "C" int qmixer_quantize(const qmixer_quantize_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_quantize_args& a = *args;
+    if (a.rows < 0 || a.heads < 1 || a.d_k < 8 || a.d_v < 8 || a.d_k % 8 || a.d_v % 8) return QSTATE_EINVAL;
+    if (a.rows > INT32_MAX || a.rows * a.heads > INT32_MAX) return QSTATE_EINVAL;
+    if (a.group < 0 || (a.group && (a.group % 8 || a.d_v % a.group))) return QSTATE_EINVAL;
+    if (a.scale_dtype != QSTATE_F16 && a.scale_dtype != QSTATE_F32) return QSTATE_EINVAL;
+    if (a.rotation != 0 && a.rotation != 1) return QSTATE_EINVAL;
+    if (a.head_bits) {
+        for (int i = 0; i < a.heads; i++)
+            if (!qm::width_ok(a.head_bits[i])) return QSTATE_EINVAL;
+    } else if (!qm::width_ok(a.bits) && a.bits != 32) {
         return QSTATE_EINVAL;
     }
-    if (!qm::aligned(S, 16) || !qm::aligned(codes, 16) || !qm::aligned(ref, 16) || !qm::aligned(scales, 4))
+    if (!qm::aligned(a.S, 16) || !qm::aligned(a.codes, 16) || !qm::aligned(a.ref, 16) || !qm::aligned(a.scales, 4))
         return QSTATE_EINVAL;
-    if ((d_k != 64 && d_k != 128) || (d_v != 64 && d_v != 128)) return QSTATE_EUNSUPPORTED;
-    if (head_bits && heads > qm::kMaxMixedHeads) return QSTATE_EUNSUPPORTED;
-    if (!rows) return QSTATE_OK;
-    if (!S || !codes || ((head_bits || bits != 32) && !scales)) return QSTATE_EINVAL;
+    if ((a.d_k != 64 && a.d_k != 128) || (a.d_v != 64 && a.d_v != 128)) return QSTATE_EUNSUPPORTED;
+    if (a.head_bits && a.heads > qm::kMaxMixedHeads) return QSTATE_EUNSUPPORTED;
+    if (!a.rows) return QSTATE_OK;
+    if (!a.S || !a.codes || ((a.head_bits || a.bits != 32) && !a.scales)) return QSTATE_EINVAL;
     qm::QuantParams p{};
-    p.S = S;
-    p.codes = static_cast<uint8_t*>(codes);
-    p.scales = scales;
-    p.ref = ref;
-    p.heads = heads;
-    p.group = group;
-    p.bits = bits;
-    p.scale_f32 = scale_dtype == QSTATE_F32;
-    p.rotate = rotation == 1;
-    p.mixed = head_bits != nullptr;
-    p.tile_bytes = (int64_t)d_k * d_v * bits / 8;
-    p.row_bytes = p.tile_bytes * heads;
-    if (head_bits) {
+    p.S = a.S;
+    p.codes = static_cast<uint8_t*>(a.codes);
+    p.scales = a.scales;
+    p.ref = a.ref;
+    p.heads = a.heads;
+    p.group = a.group;
+    p.bits = a.bits;
+    p.scale_f32 = a.scale_dtype == QSTATE_F32;
+    p.rotate = a.rotation == 1;
+    p.mixed = a.head_bits != nullptr;
+    p.tile_bytes = (int64_t)a.d_k * a.d_v * a.bits / 8;
+    p.row_bytes = p.tile_bytes * a.heads;
+    if (a.head_bits) {
         uint32_t off = 0;
-        for (int i = 0; i < heads; i++) {
-            p.head_bits[i] = head_bits[i];
+        for (int i = 0; i < a.heads; i++) {
+            p.head_bits[i] = a.head_bits[i];
             p.head_off[i] = off;
-            off += (uint32_t)(d_k * d_v * head_bits[i] / 8);
+            off += (uint32_t)(a.d_k * a.d_v * a.head_bits[i] / 8);
         }
         p.row_bytes = off;
         p.tile_bytes = 0;
     }
-    const unsigned tiles = (unsigned)(rows * heads);
+    const unsigned tiles = (unsigned)(a.rows * a.heads);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (d_k == 64 && d_v == 64) qm::quantize_kernel<64, 64><<<tiles, 256, 0, st>>>(p);
-    else if (d_k == 64) qm::quantize_kernel<64, 128><<<tiles, 256, 0, st>>>(p);
-    else if (d_v == 64) qm::quantize_kernel<128, 64><<<tiles, 256, 0, st>>>(p);
+    if (a.d_k == 64 && a.d_v == 64) qm::quantize_kernel<64, 64><<<tiles, 256, 0, st>>>(p);
+    else if (a.d_k == 64) qm::quantize_kernel<64, 128><<<tiles, 256, 0, st>>>(p);
+    else if (a.d_v == 64) qm::quantize_kernel<128, 64><<<tiles, 256, 0, st>>>(p);
     else qm::quantize_kernel<128, 128><<<tiles, 256, 0, st>>>(p);
     return qm::launched();
 }

@@ -67,8 +67,8 @@ int sm_count() {
 // chain, taken as up to four times the mean where the lengths are not known
 // here, or the whole work over the resident CTAs.  Cut: the work with launch 1
 // on top.
-ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, bool ragged, int sms) {
-    const int64_t unit = kBatchTokens;
+ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, int dtype, bool ragged, int sms) {
+    const int64_t unit = dtype == QSTATE_BF16 ? kChunk : kBatchTokens;
     const int64_t chains = (int64_t)heads * (dv / 64), resident = 2 * sms;
     const int64_t mean = tokens / sequences, longest = ragged ? (4 * mean < tokens ? 4 * mean : tokens) : mean;
     const int64_t even = tokens * chains / resident;
@@ -106,48 +106,52 @@ int64_t qmixer_scan_workspace(int32_t sequences, int64_t tokens, int32_t heads, 
     if (rc != QSTATE_OK) return rc;
     if (!sequences) return 0;
     const int sms = qm::sm_count();
-    const int64_t a = qm::scan_plan(sequences, tokens, heads, d_k, d_v, true, sms).bytes;
-    const int64_t b = qm::scan_plan(sequences, tokens, heads, d_k, d_v, false, sms).bytes;
+    const int64_t a = qm::scan_plan(sequences, tokens, heads, d_k, d_v, dtype, true, sms).bytes;
+    const int64_t b = qm::scan_plan(sequences, tokens, heads, d_k, d_v, dtype, false, sms).bytes;
     return a > b ? a : b;
 }
 
-int qmixer_scan(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const float* A, const void* B,
-                int64_t B_stride, const void* C, int64_t C_stride, const float* D, const float* dt_bias,
-                float* state, void* y, int64_t y_stride, const int32_t* seq_starts, int32_t sequences,
-                int64_t tokens, int32_t heads, int32_t groups, int32_t d_k, int32_t d_v, int32_t dtype,
-                int32_t dt_dtype, int32_t flags, void* workspace, int64_t workspace_bytes, qstate_stream stream) {
-    const int rc = qm::check_scan(sequences, tokens, heads, groups, d_k, d_v, dtype);
+int qmixer_scan(const qmixer_scan_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_scan_args& a = *args;
+    const int rc = qm::check_scan(a.sequences, a.tokens, a.heads, a.groups, a.d_k, a.d_v, a.dtype);
     if (rc == QSTATE_EINVAL) return rc;
-    if (!qm::known(dt_dtype) || (flags & ~(QMIXER_INITIAL | QMIXER_SOFTPLUS))) return QSTATE_EINVAL;
-    if (x_stride < (int64_t)heads * d_v || y_stride < (int64_t)heads * d_v || dt_stride < heads ||
-        B_stride < (int64_t)groups * d_k || C_stride < (int64_t)groups * d_k)
+    if (!qm::known(a.dt_dtype) || (a.flags & ~(QMIXER_INITIAL | QMIXER_SOFTPLUS))) return QSTATE_EINVAL;
+    if (a.x_stride < (int64_t)a.heads * a.d_v || a.y_stride < (int64_t)a.heads * a.d_v || a.dt_stride < a.heads ||
+        a.B_stride < (int64_t)a.groups * a.d_k || a.C_stride < (int64_t)a.groups * a.d_k)
         return QSTATE_EINVAL;
-    const int size = qm::size_of(dtype), unit = 16 / size;
-    if (x_stride % unit || B_stride % unit || C_stride % unit || !qm::aligned(x, 16) || !qm::aligned(B, 16) ||
-        !qm::aligned(C, 16) || !qm::aligned(state, 16) || !qm::aligned(workspace, 16) || !qm::aligned(y, size) ||
-        !qm::aligned(dt, qm::size_of(dt_dtype)) || !qm::aligned(A, 4) || !qm::aligned(D, 4) ||
-        !qm::aligned(dt_bias, 4) || !qm::aligned(seq_starts, 4))
+    const int size = qm::size_of(a.dtype), unit = 16 / size;
+    if (a.x_stride % unit || a.B_stride % unit || a.C_stride % unit || !qm::aligned(a.x, 16) || !qm::aligned(a.B, 16) ||
+        !qm::aligned(a.C, 16) || !qm::aligned(a.state, 16) || !qm::aligned(a.workspace, 16) || !qm::aligned(a.y, size) ||
+        !qm::aligned(a.dt, qm::size_of(a.dt_dtype)) || !qm::aligned(a.A, 4) || !qm::aligned(a.D, 4) ||
+        !qm::aligned(a.dt_bias, 4) || !qm::aligned(a.seq_starts, 4))
         return QSTATE_EINVAL;
-    if (!seq_starts && sequences && tokens % sequences) return QSTATE_EINVAL;
-    if ((flags & QMIXER_INITIAL) && !state && sequences) return QSTATE_EINVAL;
+    if (!a.seq_starts && a.sequences && a.tokens % a.sequences) return QSTATE_EINVAL;
+    if ((a.flags & QMIXER_INITIAL) && !a.state && a.sequences) return QSTATE_EINVAL;
     if (rc != QSTATE_OK) return rc;
-    if (!sequences || (!tokens && !state)) return QSTATE_OK;
-    if (!A || (tokens && (!x || !dt || !B || !C || !y))) return QSTATE_EINVAL;
-    const qm::ScanPlan plan = qm::scan_plan(sequences, tokens, heads, d_k, d_v, seq_starts != nullptr, qm::sm_count());
-    if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return QSTATE_EINVAL;
+    if (!a.sequences || (!a.tokens && !a.state)) return QSTATE_OK;
+    if (!a.A || (a.tokens && (!a.x || !a.dt || !a.B || !a.C || !a.y))) return QSTATE_EINVAL;
+    const qm::ScanPlan plan = qm::scan_plan(a.sequences, a.tokens, a.heads, a.d_k, a.d_v, a.dtype, a.seq_starts != nullptr, qm::sm_count());
+    if (plan.bytes && (!a.workspace || a.workspace_bytes < plan.bytes)) return QSTATE_EINVAL;
     if (plan.segments > INT32_MAX) return QSTATE_EUNSUPPORTED;
-    qm::ScanParams p{x, x_stride, dt, dt_stride, A, B, B_stride, C, C_stride, D, dt_bias, state, y, y_stride,
-                     {seq_starts, sequences, tokens, tokens / sequences}, heads, heads / groups, d_v,
-                     dt_dtype == QSTATE_BF16, (flags & QMIXER_SOFTPLUS) != 0, (flags & QMIXER_INITIAL) != 0,
-                     plan.seg_len, plan.segments, plan.cut, static_cast<float*>(workspace),
-                     plan.cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.state_bytes) : nullptr};
+    qm::ScanParams p{a.x, a.x_stride, a.dt, a.dt_stride, a.A, a.B, a.B_stride, a.C, a.C_stride, a.D, a.dt_bias, a.state, a.y, a.y_stride,
+                     {a.seq_starts, a.sequences, a.tokens, a.tokens / a.sequences}, a.heads, a.heads / a.groups, a.d_v,
+                     a.dt_dtype == QSTATE_BF16, (a.flags & QMIXER_SOFTPLUS) != 0, (a.flags & QMIXER_INITIAL) != 0,
+                     plan.seg_len, plan.segments, plan.cut, static_cast<float*>(a.workspace),
+                     plan.cut ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.state_bytes) : nullptr};
     const cudaStream_t st = (cudaStream_t)stream;
+    const bool chunked = a.dtype == QSTATE_BF16 && a.tokens > 0;
+    auto launch = [&](bool states_only) {
+        if (chunked) return qm::launch_scan_chunk(p, a.d_k, plan.segments, states_only, st);
+        qm::launch_scan_rec(p, a.dtype, a.d_k, plan.segments, states_only, st);
+        return true;
+    };
     if (plan.cut) {
-        qm::launch_scan_rec(p, dtype, d_k, plan.segments, true, st);
-        const dim3 grid((unsigned)sequences, (unsigned)heads, (unsigned)(d_k * d_v / 1024));
-        qm::join_kernel<<<grid, 256, 0, st>>>(p, d_k);
+        if (!launch(true)) return QSTATE_ECUDA;
+        const dim3 grid((unsigned)a.sequences, (unsigned)a.heads, (unsigned)(a.d_k * a.d_v / 1024));
+        qm::join_kernel<<<grid, 256, 0, st>>>(p, a.d_k);
     }
-    qm::launch_scan_rec(p, dtype, d_k, plan.segments, false, st);
+    if (!launch(false)) return QSTATE_ECUDA;
     return qm::launched();
 }
 

@@ -40,7 +40,8 @@ struct ScanParams {
     float* seg_decay;           // [segments][heads]
 };
 
-constexpr int kBatchTokens = 16;   // segments are whole batches of the recurrent form
+constexpr int kBatchTokens = 16;   // the recurrent form's segments are whole batches,
+constexpr int kChunk = 128;        // the chunked form's whole chunks
 
 struct Segment {
     int sequence;
@@ -101,5 +102,6 @@ __device__ __forceinline__ bool find_segment(const ScanParams& p, int64_t g, Seg
 // The kernels of the recurrent form (any type) and of the chunked form
 // (bfloat16, tensor cores): states only (launch 1) or the whole scan.
 void launch_scan_rec(const ScanParams& p, int dtype, int dk, int64_t segments, bool states_only, cudaStream_t st);
+bool launch_scan_chunk(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
 
 }  // namespace qm

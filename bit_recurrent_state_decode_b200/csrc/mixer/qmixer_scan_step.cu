@@ -159,72 +159,69 @@ int check_step(const void* x, int64_t xs, const void* dt, int64_t dts, const flo
 
 extern "C" {
 
-int qmixer_scan_step(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const float* A,
-                     const void* B, int64_t B_stride, const void* C, int64_t C_stride, const float* D,
-                     const float* dt_bias, float* state, void* y, int64_t y_stride, int32_t batch, int32_t heads,
-                     int32_t groups, int32_t d_k, int32_t d_v, int32_t dtype, int32_t dt_dtype, int32_t flags,
-                     qstate_stream stream) {
-    const int rc = qm::check_step(x, x_stride, dt, dt_stride, A, B, B_stride, C, C_stride, batch, heads, groups, d_k,
-                                  d_v, dtype, dt_dtype, flags);
+int qmixer_scan_step(const qmixer_scan_step_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_scan_step_args& a = *args;
+    const int rc = qm::check_step(a.x, a.x_stride, a.dt, a.dt_stride, a.A, a.B, a.B_stride, a.C, a.C_stride, a.batch, a.heads, a.groups, a.d_k,
+                                  a.d_v, a.dtype, a.dt_dtype, a.flags);
     if (rc != QSTATE_OK) return rc;
-    if (y_stride < (int64_t)heads * d_v || !qm::aligned(state, 16) || !qm::aligned(y, qm::size_of(dtype)) ||
-        !qm::aligned(D, 4) || !qm::aligned(dt_bias, 4))
+    if (a.y_stride < (int64_t)a.heads * a.d_v || !qm::aligned(a.state, 16) || !qm::aligned(a.y, qm::size_of(a.dtype)) ||
+        !qm::aligned(a.D, 4) || !qm::aligned(a.dt_bias, 4))
         return QSTATE_EINVAL;
-    if (!batch) return QSTATE_OK;
-    if (!state || !y) return QSTATE_EINVAL;
-    const qm::StepParams p{x, x_stride, dt, dt_stride, A, B, B_stride, C, C_stride, D, dt_bias, state, y, y_stride,
-                           heads, heads / groups, dt_dtype == QSTATE_BF16, (flags & QMIXER_SOFTPLUS) != 0};
-    if (dtype == QSTATE_BF16) qm::launch_scan_step<qm::bf16>(p, (int64_t)batch * heads, d_k, d_v, (cudaStream_t)stream);
-    else qm::launch_scan_step<float>(p, (int64_t)batch * heads, d_k, d_v, (cudaStream_t)stream);
+    if (!a.batch) return QSTATE_OK;
+    if (!a.state || !a.y) return QSTATE_EINVAL;
+    const qm::StepParams p{a.x, a.x_stride, a.dt, a.dt_stride, a.A, a.B, a.B_stride, a.C, a.C_stride, a.D, a.dt_bias, a.state, a.y, a.y_stride,
+                           a.heads, a.heads / a.groups, a.dt_dtype == QSTATE_BF16, (a.flags & QMIXER_SOFTPLUS) != 0};
+    if (a.dtype == QSTATE_BF16) qm::launch_scan_step<qm::bf16>(p, (int64_t)a.batch * a.heads, a.d_k, a.d_v, (cudaStream_t)stream);
+    else qm::launch_scan_step<float>(p, (int64_t)a.batch * a.heads, a.d_k, a.d_v, (cudaStream_t)stream);
     return qm::launched();
 }
 
-int qmixer_step_operands(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const float* A,
-                         const void* B, int64_t B_stride, const void* C, int64_t C_stride, const float* dt_bias,
-                         void* q, void* k, void* v, void* gates, int32_t batch, int32_t heads, int32_t groups,
-                         int32_t d_k, int32_t d_v, int32_t dtype, int32_t dt_dtype, int32_t qkv_dtype,
-                         int32_t gate_dtype, int32_t flags, qstate_stream stream) {
-    const int rc = qm::check_step(x, x_stride, dt, dt_stride, A, B, B_stride, C, C_stride, batch, heads, groups, d_k,
-                                  d_v, dtype, dt_dtype, flags);
+int qmixer_step_operands(const qmixer_step_operands_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_step_operands_args& a = *args;
+    const int rc = qm::check_step(a.x, a.x_stride, a.dt, a.dt_stride, a.A, a.B, a.B_stride, a.C, a.C_stride, a.batch, a.heads, a.groups, a.d_k,
+                                  a.d_v, a.dtype, a.dt_dtype, a.flags);
     if (rc != QSTATE_OK) return rc;
-    if (!qm::known(qkv_dtype) || !qm::known(gate_dtype) || !qm::aligned(dt_bias, 4)) return QSTATE_EINVAL;
-    if (!qm::aligned(q, 4) || !qm::aligned(k, 4) || !qm::aligned(v, 4) || !qm::aligned(gates, 4)) return QSTATE_EINVAL;
-    if (!batch) return QSTATE_OK;
-    if (!q || !k || !v || !gates) return QSTATE_EINVAL;
+    if (!qm::known(a.qkv_dtype) || !qm::known(a.gate_dtype) || !qm::aligned(a.dt_bias, 4)) return QSTATE_EINVAL;
+    if (!qm::aligned(a.q, 4) || !qm::aligned(a.k, 4) || !qm::aligned(a.v, 4) || !qm::aligned(a.gates, 4)) return QSTATE_EINVAL;
+    if (!a.batch) return QSTATE_OK;
+    if (!a.q || !a.k || !a.v || !a.gates) return QSTATE_EINVAL;
     qm::OperandParams p{};
-    p.s = {x, x_stride, dt, dt_stride, A, B, B_stride, C, C_stride, nullptr, dt_bias, nullptr, nullptr, 0,
-           heads, heads / groups, dt_dtype == QSTATE_BF16, (flags & QMIXER_SOFTPLUS) != 0};
-    p.q = q;
-    p.k = k;
-    p.v = v;
-    p.gates = gates;
-    p.tiles = (int64_t)batch * heads;
-    p.dk = d_k;
-    p.dv = d_v;
-    p.out_bf16 = qkv_dtype == QSTATE_BF16;
-    p.gate_bf16 = gate_dtype == QSTATE_BF16;
-    if (dtype == QSTATE_BF16) qm::operands_kernel<qm::bf16><<<(unsigned)p.tiles, 128, 0, (cudaStream_t)stream>>>(p);
+    p.s = {a.x, a.x_stride, a.dt, a.dt_stride, a.A, a.B, a.B_stride, a.C, a.C_stride, nullptr, a.dt_bias, nullptr, nullptr, 0,
+           a.heads, a.heads / a.groups, a.dt_dtype == QSTATE_BF16, (a.flags & QMIXER_SOFTPLUS) != 0};
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.gates = a.gates;
+    p.tiles = (int64_t)a.batch * a.heads;
+    p.dk = a.d_k;
+    p.dv = a.d_v;
+    p.out_bf16 = a.qkv_dtype == QSTATE_BF16;
+    p.gate_bf16 = a.gate_dtype == QSTATE_BF16;
+    if (a.dtype == QSTATE_BF16) qm::operands_kernel<qm::bf16><<<(unsigned)p.tiles, 128, 0, (cudaStream_t)stream>>>(p);
     else qm::operands_kernel<float><<<(unsigned)p.tiles, 128, 0, (cudaStream_t)stream>>>(p);
     return qm::launched();
 }
 
-int qmixer_step_output(const float* out, const void* x, int64_t x_stride, const float* D, void* y, int64_t y_stride,
-                       int32_t batch, int32_t heads, int32_t d_v, int32_t dtype, qstate_stream stream) {
-    if (!qm::known(dtype) || batch < 0 || heads < 1 || d_v < 1) return QSTATE_EINVAL;
-    const int64_t row = (int64_t)heads * d_v, n = batch * row;
-    if (row > INT32_MAX || y_stride < row || (D && x_stride < row)) return QSTATE_EINVAL;
-    const int size = qm::size_of(dtype);
-    if (!qm::aligned(out, 4) || !qm::aligned(D, 4) || !qm::aligned(x, size) || !qm::aligned(y, size)) return QSTATE_EINVAL;
+int qmixer_step_output(const qmixer_step_output_args* args, qstate_stream stream) {
+    if (!args) return QSTATE_EINVAL;
+    const qmixer_step_output_args& a = *args;
+    if (!qm::known(a.dtype) || a.batch < 0 || a.heads < 1 || a.d_v < 1) return QSTATE_EINVAL;
+    const int64_t row = (int64_t)a.heads * a.d_v, n = a.batch * row;
+    if (row > INT32_MAX || a.y_stride < row || (a.D && a.x_stride < row)) return QSTATE_EINVAL;
+    const int size = qm::size_of(a.dtype);
+    if (!qm::aligned(a.out, 4) || !qm::aligned(a.D, 4) || !qm::aligned(a.x, size) || !qm::aligned(a.y, size)) return QSTATE_EINVAL;
     if (!n) return QSTATE_OK;
-    if (!out || !y || (D && !x)) return QSTATE_EINVAL;
+    if (!a.out || !a.y || (a.D && !a.x)) return QSTATE_EINVAL;
     if ((n + 255) / 256 > INT32_MAX) return QSTATE_EUNSUPPORTED;
     const unsigned blocks = (unsigned)((n + 255) / 256);
-    if (dtype == QSTATE_BF16)
-        qm::output_kernel<<<blocks, 256, 0, (cudaStream_t)stream>>>(out, (const qm::bf16*)x, x_stride, D, (qm::bf16*)y,
-                                                                    y_stride, n, heads, d_v);
+    if (a.dtype == QSTATE_BF16)
+        qm::output_kernel<<<blocks, 256, 0, (cudaStream_t)stream>>>(a.out, (const qm::bf16*)a.x, a.x_stride, a.D, (qm::bf16*)a.y,
+                                                                    a.y_stride, n, a.heads, a.d_v);
     else
-        qm::output_kernel<<<blocks, 256, 0, (cudaStream_t)stream>>>(out, (const float*)x, x_stride, D, (float*)y,
-                                                                    y_stride, n, heads, d_v);
+        qm::output_kernel<<<blocks, 256, 0, (cudaStream_t)stream>>>(a.out, (const float*)a.x, a.x_stride, a.D, (float*)a.y,
+                                                                    a.y_stride, n, a.heads, a.d_v);
     return qm::launched();
 }
 

@@ -17,7 +17,9 @@ gradient are refused while gradients are recorded.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -31,9 +33,13 @@ INITIAL, SILU, SOFTPLUS = 1, 2, 4
 BEFORE_NONE, BEFORE_RESIDUAL, BEFORE_GATE = 0, 1, 2
 OUT_SAME, OUT_INT8, OUT_E4M3 = 0, 1, 2
 
-# every symbol include/qmixer.h declares
-EXPORTS = ("qmixer_conv", "qmixer_conv_step", "qmixer_scan", "qmixer_scan_workspace", "qmixer_scan_step",
-           "qmixer_step_operands", "qmixer_step_output", "qmixer_norm", "qmixer_quantize")
+# every function include/qmixer.h declares, with the fields of its argument
+# structure in the notation of the struct module (native alignment)
+_FIELDS = {"qmixer_conv": "PqPPPPqPiqiiii", "qmixer_conv_step": "PqPPPPqiiiii",
+           "qmixer_scan": "PqPqPPqPqPPPPqPiqiiiiiiiPq", "qmixer_scan_step": "PqPqPPqPqPPPPqiiiiiiii",
+           "qmixer_step_operands": "PqPqPPqPqPPPPPiiiiiiiiii", "qmixer_step_output": "PPqPPqiiii",
+           "qmixer_norm": "PqPqPPqPqiifiii", "qmixer_quantize": "PPPPqiiiiPiii"}
+EXPORTS = tuple(_FIELDS) + ("qmixer_scan_workspace",)
 
 _lib = None
 
@@ -46,98 +52,103 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m bit_recurrent_state_decode_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
-        P, I, L64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-        row = [P, L64]
-        L.qmixer_conv.argtypes = row + [P, P, P] + row + [P, I, L64, I, I, I, I, P]
-        L.qmixer_conv_step.argtypes = row + [P, P, P] + row + [I, I, I, I, I, P]
-        ops = row + row + [P] + row + row
-        L.qmixer_scan.argtypes = ops + [P, P, P] + row + [P, I, L64, I, I, I, I, I, I, I, P, L64, P]
-        L.qmixer_scan_workspace.argtypes = [I, L64, I, I, I, I, I]
-        L.qmixer_scan_step.argtypes = ops + [P, P, P] + row + [I, I, I, I, I, I, I, I, P]
-        L.qmixer_step_operands.argtypes = ops + [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P]
-        L.qmixer_step_output.argtypes = [P] + row + [P] + row + [I, I, I, I, P]
-        L.qmixer_norm.argtypes = row + row + [P] + row + [P, L64, I, I, F, I, I, I, P]
-        L.qmixer_quantize.argtypes = [P, P, P, P, L64, I, I, I, I, P, I, I, I, P]
-        for name in EXPORTS:
-            getattr(L, name).restype = I
-        L.qmixer_scan_workspace.restype = L64
+        for name in _FIELDS:
+            f = getattr(L, name)
+            f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
+        L.qmixer_scan_workspace.argtypes = [ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 5
+        L.qmixer_scan_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
 
 
-def _check(fn, rc):
-    if rc != Q.OK:
-        raise QStateError(fn, rc)
+def _entry(name):
+    """The C call `name` of an argument structure's fields (addresses as integers, 0
+    for NULL) and a stream.  The structure is packed into bytes in one go: a
+    ctypes conversion of each field would cost as much as a small kernel."""
+    pack = struct.Struct(_FIELDS[name]).pack
+
+    def call(stream, *fields):
+        rc = getattr(_lib or lib(), name)(pack(*fields), stream)
+        if rc:
+            raise QStateError(name, rc)
+    return call
+
+
+_conv, _conv_step, _scan, _scan_step, _step_operands, _step_output, _norm, _quantize = map(_entry, _FIELDS)
 
 
 # ---------------------------------------------------------------- argument checks
 _CODE = {torch.float32: Q.F32, torch.bfloat16: Q.BF16}
+_F32 = torch.float32
+# address of a device's current stream (torch.cuda.current_stream builds an object first)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _tensor(fn, name, t, like=None, dtype=None, shape=None):
-    """A CUDA tensor of the given device, type and shape that no gradient is wanted for."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _tensor(fn, name, t, index, dtype=None, shape=None):
+    """Refuse what is not a CUDA tensor of this device (None: any), type and shape
+    (None: any), or wants a gradient."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on {like.device}")
-    if dtype is not None and t.dtype != dtype:
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on cuda:{index}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{fn}: {name} requires a gradient, and {fn} has no backward pass")
-    return t
 
 
-def _dense(fn, name, t, like, dtype, shape):
-    _tensor(fn, name, t, like, dtype, shape)
+def _dense(fn, name, t, index, dtype, shape):
+    """The same for a contiguous tensor; returns its address."""
+    _tensor(fn, name, t, index, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous")
-    return t
+    return t.data_ptr()
 
 
 def _rows(fn, name, t, inner):
-    """(address, stride between rows) of a tensor whose last `inner` dimensions are
-    contiguous and whose leading ones, where there are two, walk in one stride."""
+    """Stride between the rows of a tensor whose last `inner` dimensions are a row:
+    contiguous, the leading ones (one or two) walking in one stride."""
+    shape, strides = t.shape, t.stride()
     step = 1
-    for d in range(t.dim() - 1, t.dim() - 1 - inner, -1):
-        if t.shape[d] != 1 and t.stride(d) != step:
+    for d in range(len(shape) - 1, len(shape) - 1 - inner, -1):
+        if strides[d] != step and shape[d] != 1:
             raise ValueError(f"{fn}: the elements of a row of {name} must be contiguous")
-        step *= t.shape[d]
-    lead = t.dim() - inner
-    n = t.shape[lead - 1]
-    stride = t.stride(lead - 1) if n > 1 else step
-    if lead == 2 and t.shape[0] > 1:
+        step *= shape[d]
+    at = len(shape) - inner - 1
+    n = shape[at]
+    stride = strides[at] if n > 1 else step
+    if at == 1 and shape[0] > 1:
         if n == 1:
-            stride = t.stride(0)
-        elif n and t.stride(0) != n * stride:
+            stride = strides[0]
+        elif n > 1 and strides[0] != n * stride:
             raise ValueError(f"{fn}: the sequences of {name} must lie one behind the other")
-    return t.data_ptr(), max(stride, step) if t.numel() == 0 or lead == 0 else stride
-
-
-def _overlap(fn, name, a, other, b):
-    """Refuse an output that shares memory with an input."""
-    if a.numel() and b.numel():
-        a0, b0 = a.data_ptr(), b.data_ptr()
-        if a0 < b0 + _span(b) and b0 < a0 + _span(a):
-            # rows of one buffer may interleave without sharing an element
-            if not _interleaved(a, b):
-                raise ValueError(f"{fn}: {name} overlaps {other}")
+    if n and stride < step:
+        raise ValueError(f"{fn}: the rows of {name} overlap")
+    return stride
 
 
 def _span(t):
-    return (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size()
+    return (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size() if t.numel() else 0
 
 
-def _interleaved(a, b):
-    """Two views of rows of one pitch whose columns are apart."""
-    pa, pb = a.stride(0) * a.element_size(), b.stride(0) * b.element_size()
-    if pa != pb or a.dim() < 2 or b.dim() < 2:
-        return False
-    wa = _span(a[0]) if a.shape[0] else 0
-    wb = _span(b[0]) if b.shape[0] else 0
-    off = (b.data_ptr() - a.data_ptr()) % pa if pa else 0
-    return off >= wa and off + wb <= pa
+def _apart(fn, name, a, other, b):
+    """Refuse an output that shares memory with an input; columns of one buffer's
+    rows may interleave."""
+    if b is None:
+        return
+    pa, pb = a.data_ptr(), b.data_ptr()
+    if pa >= pb + _span(b) or pb >= pa + _span(a):
+        return
+    if a.dim() > 1 and b.dim() > 1:
+        pitch = a.stride(0) * a.element_size()
+        if pitch and pitch == b.stride(0) * b.element_size():
+            off = (pb - pa) % pitch
+            if off >= _span(a[0]) and off + _span(b[0]) <= pitch:
+                return
+    raise ValueError(f"{fn}: {name} overlaps {other}")
 
 
 def _code(fn, t):
@@ -147,49 +158,30 @@ def _code(fn, t):
     return c
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-class _On:
-    """The device of `t` and the stream to launch on; allocations inside belong to that stream."""
-
-    def __init__(self, t, stream):
-        i = t.device.index
-        self.guard = self.side = None
-        if i != torch.cuda.current_device():
-            self.guard = torch.cuda.device(i)
+def _launch(fn, t, stream, body):
+    """body(address of the stream) with the tensors' device current, and, on a
+    stream of the caller's, its allocations belonging to that stream."""
+    index = t.get_device()
+    if stream is None and index == torch.cuda.current_device():
+        return body(_raw_stream(index))
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.device(index):
         if stream is None:
-            self.stream = None
-        else:
-            if stream.device.index != i:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-            self.side = torch.cuda.stream(stream)
-        self.index = i
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.side is not None:
-            self.side.__enter__()
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *a):
-        if self.side is not None:
-            self.side.__exit__(*a)
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+            return body(_raw_stream(index))
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
 
 
-def _sequences(fn, lead, seq_starts, like):
+def _sequences(fn, lead, seq_starts, index):
     """(sequences, tokens, address of seq_starts) of a prompt's leading dimensions."""
     if len(lead) == 2:
         if seq_starts is not None:
             raise ValueError(f"{fn}: seq_starts goes with tokens in one axis, not with a batch of equal sequences")
-        return lead[0], lead[0] * lead[1], None
+        return lead[0], lead[0] * lead[1], 0
     if seq_starts is None:
-        return 1, lead[0], None
-    _tensor(fn, "seq_starts", seq_starts, like, torch.int32)
+        return 1, lead[0], 0
+    _tensor(fn, "seq_starts", seq_starts, index, torch.int32)
     if seq_starts.dim() != 1 or seq_starts.numel() < 1 or not seq_starts.is_contiguous():
         raise ValueError(f"{fn}: seq_starts must be a contiguous vector of the sequences' first tokens and their end")
     return seq_starts.numel() - 1, lead[0], seq_starts.data_ptr()
@@ -197,11 +189,12 @@ def _sequences(fn, lead, seq_starts, like):
 
 def _out(fn, out, like, shape, dtype, inputs):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _tensor(fn, "out", out, like, dtype, tuple(shape))
+        if dtype is like.dtype and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
+    _tensor(fn, "out", out, like.get_device(), dtype, shape)
     for name, t in inputs:
-        if t is not None:
-            _overlap(fn, "out", out, name, t)
+        _apart(fn, "out", out, name, t)
     return out
 
 
@@ -218,79 +211,102 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
     Tokens behind the last sequence stay as they are in `out` (undefined where
     `out` is not given).  Returns out, shaped like x."""
     fn = "conv"
-    _tensor(fn, "x", x)
+    _tensor(fn, "x", x, None)
     if x.dim() not in (2, 3):
         raise ValueError(f"{fn}: x must be [batch, length, channels] or [tokens, channels]")
-    code = _code(fn, x)
-    n, tokens, starts = _sequences(fn, x.shape[:-1], seq_starts, x)
-    channels = x.shape[-1]
-    width = _taps(fn, x, weight, bias, state, n)
+    shape, index, code = x.shape, x.get_device(), _code(fn, x)
+    n, tokens, starts = _sequences(fn, shape[:-1], seq_starts, index)
+    width, wp, bp, sp = _taps(fn, x, weight, bias, state, n, index)
     if initial and state is None:
         raise ValueError(f"{fn}: initial=True needs the state to continue from")
-    xp, xs = _rows(fn, "x", x, 1)
-    with _On(x, stream) as st:
-        y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
-        yp, ys = _rows(fn, "out", y, 1)
-        _check("qmixer_conv", lib().qmixer_conv(
-            xp, xs, weight.data_ptr(), _ptr(bias), _ptr(state), yp, ys, starts, n, tokens, channels, width, code,
-            (INITIAL if initial else 0) | (SILU if activation else 0), st))
-    return y
+    xs = _rows(fn, "x", x, 1)
+
+    def body(st):
+        y = _out(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
+        _conv(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), _rows(fn, "out", y, 1), starts, n, tokens, shape[-1],
+              width, code, (INITIAL if initial else 0) | (SILU if activation else 0))
+        return y
+    return _launch(fn, x, stream, body)
 
 
 def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=None):
     """The same for one token of each sequence: x [batch, channels]; state
     [batch, width - 1, channels] moves on by one token."""
     fn = "conv_step"
-    _tensor(fn, "x", x)
+    _tensor(fn, "x", x, None)
     if x.dim() != 2:
         raise ValueError(f"{fn}: x must be [batch, channels]")
-    code = _code(fn, x)
     if state is None:
         raise ValueError(f"{fn}: state is required")
-    width = _taps(fn, x, weight, bias, state, x.shape[0])
-    xp, xs = _rows(fn, "x", x, 1)
-    with _On(x, stream) as st:
-        y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
-        yp, ys = _rows(fn, "out", y, 1)
-        _check("qmixer_conv_step", lib().qmixer_conv_step(
-            xp, xs, weight.data_ptr(), _ptr(bias), _ptr(state), yp, ys, x.shape[0], x.shape[1], width, code,
-            SILU if activation else 0, st))
-    return y
+    shape, code = x.shape, _code(fn, x)
+    width, wp, bp, sp = _taps(fn, x, weight, bias, state, shape[0], x.get_device())
+    xs = _rows(fn, "x", x, 1)
+
+    def body(st):
+        y = _out(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
+        _conv_step(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), _rows(fn, "out", y, 1), shape[0], shape[1], width,
+                   code, SILU if activation else 0)
+        return y
+    return _launch(fn, x, stream, body)
 
 
-def _taps(fn, x, weight, bias, state, n):
-    channels = x.shape[-1]
-    _tensor(fn, "weight", weight, x, x.dtype)
+def _taps(fn, x, weight, bias, state, n, index):
+    channels, dtype = x.shape[-1], x.dtype
+    _tensor(fn, "weight", weight, index, dtype)
     if weight.dim() != 2 or weight.shape[0] != channels or not weight.is_contiguous():
         raise ValueError(f"{fn}: weight must be contiguous [channels, width]")
     width = weight.shape[1]
-    if bias is not None:
-        _dense(fn, "bias", bias, x, x.dtype, (channels,))
+    bp = 0 if bias is None else _dense(fn, "bias", bias, index, dtype, (channels,))
+    sp = 0
     if state is not None:
-        _dense(fn, "state", state, x, x.dtype, (n, width - 1, channels))
-        _overlap(fn, "state", state, "x", x)
-    return width
+        sp = _dense(fn, "state", state, index, dtype, (n, width - 1, channels))
+        end, at = sp + state.nbytes, x.data_ptr()
+        if at < end and sp < at + _span(x):
+            _apart(fn, "state", state, "x", x)
+    return width, weight.data_ptr(), bp, sp
 
 
 # ---------------------------------------------------------------- selective scan
 def _selective(fn, x, dt, A, B, C, D, dt_bias):
-    _tensor(fn, "x", x)
-    code = _code(fn, x)
-    lead, (heads, d_v) = tuple(x.shape[:-2]), x.shape[-2:]
-    _tensor(fn, "dt", dt, x, None, lead + (heads,))
-    dt_code = _code(fn, dt)
-    _tensor(fn, "B", B, x, x.dtype)
-    if B.dim() != x.dim() or tuple(B.shape[:-2]) != lead:
-        raise ValueError(f"{fn}: B has shape {tuple(B.shape)}, expected {lead} + (groups, d_k)")
-    groups, d_k = B.shape[-2:]
-    _tensor(fn, "C", C, x, x.dtype, tuple(B.shape))
+    """The fields x, dt, A, B, C and D, dt_bias of a call, then (dtype, dt's dtype,
+    heads, groups, d_k, d_v) and the device."""
+    _tensor(fn, "x", x, None)
+    code, index, xsh, dtype = _code(fn, x), x.get_device(), x.shape, x.dtype
+    heads, d_v = xsh[-2], xsh[-1]
+    _tensor(fn, "dt", dt, index, None, xsh[:-1])
+    _tensor(fn, "B", B, index, dtype)
+    bsh = B.shape
+    if len(bsh) != len(xsh) or bsh[:-2] != xsh[:-2]:
+        raise ValueError(f"{fn}: B has shape {tuple(bsh)}, expected {tuple(xsh[:-2])} + (groups, d_k)")
+    groups, d_k = bsh[-2], bsh[-1]
+    _tensor(fn, "C", C, index, dtype, bsh)
     if groups == 0 or heads % groups:
         raise ValueError(f"{fn}: {heads} heads do not divide into {groups} groups")
-    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-        if t is not None or name == "A":
-            _dense(fn, name, t, x, torch.float32, (heads,))
-    rows = (*_rows(fn, "x", x, 2), *_rows(fn, "dt", dt, 1), A.data_ptr(), *_rows(fn, "B", B, 2), *_rows(fn, "C", C, 2))
-    return rows, code, dt_code, heads, groups, d_k, d_v
+    per_head = (heads,)
+    rows = (x.data_ptr(), _rows(fn, "x", x, 2), dt.data_ptr(), _rows(fn, "dt", dt, 1),
+            _dense(fn, "A", A, index, _F32, per_head), B.data_ptr(), _rows(fn, "B", B, 2), C.data_ptr(),
+            _rows(fn, "C", C, 2))
+    return (rows, 0 if D is None else _dense(fn, "D", D, index, _F32, per_head),
+            0 if dt_bias is None else _dense(fn, "dt_bias", dt_bias, index, _F32, per_head),
+            (heads, groups, d_k, d_v, code, _code(fn, dt)), index)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(index, *sizes):
+    """qmixer_scan_workspace of a device, which has to be the current one."""
+    size = lib().qmixer_scan_workspace(*sizes)
+    if size < 0:
+        raise QStateError("qmixer_scan", size)
+    return size
+
+
+def _states_apart(fn, state, sp, rows, x, dt, B, C):
+    """_apart of the states and the inputs, by bounds first."""
+    end, reach = sp + state.nbytes, x.shape[:-2].numel() * 4
+    for i, name, t in ((0, "x", x), (2, "dt", dt), (5, "B", B), (7, "C", C)):
+        at = rows[i]
+        if at < end and sp < at + reach * rows[i + 1]:
+            _apart(fn, "state", state, name, t)
 
 
 def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, initial=False, seq_starts=None,
@@ -310,23 +326,24 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
     fn = "scan"
     if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError(f"{fn}: x must be [batch, length, heads, d_v] or [tokens, heads, d_v]")
-    rows, code, dt_code, heads, groups, d_k, d_v = _selective(fn, x, dt, A, B, C, D, dt_bias)
-    n, tokens, starts = _sequences(fn, x.shape[:-2], seq_starts, x)
+    rows, dp, biasp, sizes, index = _selective(fn, x, dt, A, B, C, D, dt_bias)
+    n, tokens, starts = _sequences(fn, x.shape[:-2], seq_starts, index)
     if initial and state is None:
         raise ValueError(f"{fn}: initial=True needs the state to continue from")
+    heads, groups, d_k, d_v = sizes[:4]
+    sp = 0
     if state is not None:
-        _dense(fn, "state", state, x, torch.float32, (n, heads, d_k, d_v))
-    with _On(x, stream) as st:
+        sp = _dense(fn, "state", state, index, _F32, (n, heads, d_k, d_v))
+        _states_apart(fn, state, sp, rows, x, dt, B, C)
+
+    def body(st):
         y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
-        yp, ys = _rows(fn, "out", y, 2)
-        size = lib().qmixer_scan_workspace(n, tokens, heads, groups, d_k, d_v, code)
-        if size < 0:
-            raise QStateError("qmixer_scan", size)
-        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
-        _check("qmixer_scan", lib().qmixer_scan(
-            *rows, _ptr(D), _ptr(dt_bias), _ptr(state), yp, ys, starts, n, tokens, heads, groups, d_k, d_v, code,
-            dt_code, (INITIAL if initial else 0) | (SOFTPLUS if softplus else 0), _ptr(work), size, st))
-    return y
+        size = _workspace(index, n, tokens, *sizes[:5])
+        work = x.new_empty(size, dtype=torch.uint8) if size else None
+        _scan(st, *rows, dp, biasp, sp, y.data_ptr(), _rows(fn, "out", y, 2), starts, n, tokens, *sizes,
+              (INITIAL if initial else 0) | (SOFTPLUS if softplus else 0), work.data_ptr() if size else 0, size)
+        return y
+    return _launch(fn, x, stream, body)
 
 
 def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out=None, stream=None):
@@ -335,16 +352,18 @@ def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out
     fn = "scan_step"
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{fn}: x must be [batch, heads, d_v]")
-    rows, code, dt_code, heads, groups, d_k, d_v = _selective(fn, x, dt, A, B, C, D, dt_bias)
-    n = x.shape[0]
-    _dense(fn, "state", state, x, torch.float32, (n, heads, d_k, d_v))
-    with _On(x, stream) as st:
-        y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
-        yp, ys = _rows(fn, "out", y, 2)
-        _check("qmixer_scan_step", lib().qmixer_scan_step(
-            *rows, _ptr(D), _ptr(dt_bias), state.data_ptr(), yp, ys, n, heads, groups, d_k, d_v, code, dt_code,
-            SOFTPLUS if softplus else 0, st))
-    return y
+    rows, dp, biasp, sizes, index = _selective(fn, x, dt, A, B, C, D, dt_bias)
+    shape = x.shape
+    n = shape[0]
+    sp = _dense(fn, "state", state, index, _F32, (n, sizes[0], sizes[2], sizes[3]))
+    _states_apart(fn, state, sp, rows, x, dt, B, C)
+
+    def body(st):
+        y = _out(fn, out, x, shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
+        _scan_step(st, *rows, dp, biasp, sp, y.data_ptr(), _rows(fn, "out", y, 2), n, *sizes,
+                   SOFTPLUS if softplus else 0)
+        return y
+    return _launch(fn, x, stream, body)
 
 
 # ---------------------------------------------------------------- the low-bit state
@@ -357,25 +376,29 @@ def load(obj, S, *, stream=None):
     fn = "load"
     if getattr(obj, "rowcol", False):
         raise ValueError(f"{fn}: an object with row x column scales fits them in its own steps only")
-    _tensor(fn, "S", S, None, torch.float32)
-    if S.device.index != obj.device:
+    _tensor(fn, "S", S, None, _F32)
+    if S.get_device() != obj.device:
         raise ValueError(f"{fn}: S is on {S.device}, the object on cuda:{obj.device}")
-    if S.numel() != obj.tiles * obj.d_k * obj.d_v or tuple(S.shape[-2:]) != (obj.d_k, obj.d_v):
+    if S.numel() != obj.tiles * obj.d_k * obj.d_v or S.shape[-2:] != (obj.d_k, obj.d_v):
         raise ValueError(f"{fn}: S has shape {tuple(S.shape)}, the object {obj.tiles} tiles of {obj.d_k} x {obj.d_v}")
     if not S.is_contiguous():
         raise ValueError(f"{fn}: S must be contiguous")
     if obj.tiles == 0:
         return
     z = obj.sizes
-    hb = None if obj.head_bits is None else (ctypes.c_uint8 * obj.heads)(*obj.head_bits)
-    with _On(S, stream) as st:
-        codes = torch.empty(z["code_bytes"], dtype=torch.uint8, device=S.device)
-        scales = torch.empty(max(z["scale_bytes"], 4), dtype=torch.uint8, device=S.device)
+
+    def body(st):
+        # an object's own buffers are reached by qstate_import alone
+        codes = S.new_empty(z["code_bytes"], dtype=torch.uint8)
+        scales = S.new_empty(max(z["scale_bytes"], 4), dtype=torch.uint8)
         ref = torch.empty_like(S) if z["ref_bytes"] else None
-        _check("qmixer_quantize", lib().qmixer_quantize(
-            S.data_ptr(), codes.data_ptr(), scales.data_ptr(), _ptr(ref), obj.layers * obj.batch, obj.heads, obj.d_k,
-            obj.d_v, 0 if hb is not None else obj.bits, hb, obj.group, obj.scale_dtype, obj.rotation, st))
+        mixed = obj.head_bits is not None
+        hb = (ctypes.c_uint8 * obj.heads)(*obj.head_bits) if mixed else None
+        _quantize(st, S.data_ptr(), codes.data_ptr(), scales.data_ptr(), 0 if ref is None else ref.data_ptr(),
+                  obj.layers * obj.batch, obj.heads, obj.d_k, obj.d_v, 0 if mixed else obj.bits,
+                  ctypes.addressof(hb) if mixed else 0, obj.group, obj.scale_dtype, obj.rotation)
         obj.import_(codes, scales, ref, stream=torch.cuda.current_stream())
+    _launch(fn, S, stream, body)
 
 
 def step(obj, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, out=None, stream=None):
@@ -387,26 +410,26 @@ def step(obj, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, out=None, 
         raise ValueError(f"{fn}: x must be [batch, heads, d_v]")
     if obj.kind != Q.MAMBA2 or obj.layers != 1:
         raise ValueError(f"{fn}: the object must be of kind MAMBA2 and hold one layer")
-    rows, code, dt_code, heads, groups, d_k, d_v = _selective(fn, x, dt, A, B, C, D, dt_bias)
+    rows, dp, biasp, sizes, index = _selective(fn, x, dt, A, B, C, D, dt_bias)
     n = x.shape[0]
-    if (n, heads, d_k, d_v) != (obj.batch, obj.heads, obj.d_k, obj.d_v):
-        raise ValueError(f"{fn}: the operands are {n} x {heads} tiles of {d_k} x {d_v}, the object "
+    if (n, sizes[0], sizes[2], sizes[3]) != (obj.batch, obj.heads, obj.d_k, obj.d_v):
+        raise ValueError(f"{fn}: the operands are {n} x {sizes[0]} tiles of {sizes[2]} x {sizes[3]}, the object "
                          f"{obj.batch} x {obj.heads} of {obj.d_k} x {obj.d_v}")
-    if x.device.index != obj.device:
+    if index != obj.device:
         raise ValueError(f"{fn}: x is on {x.device}, the object on cuda:{obj.device}")
-    with _On(x, stream) as st:
+
+    def body(st):
         y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt)))
-        yp, ys = _rows(fn, "out", y, 2)
         if n == 0:
             return y
         q, k, v, gates, o = obj.alloc_inputs(x.device)
-        _check("qmixer_step_operands", lib().qmixer_step_operands(
-            *rows, _ptr(dt_bias), q.data_ptr(), k.data_ptr(), v.data_ptr(), gates.data_ptr(), n, heads, groups, d_k,
-            d_v, code, dt_code, obj.qkv_dtype, obj.gate_dtype, SOFTPLUS if softplus else 0, st))
+        _step_operands(st, *rows, biasp, q.data_ptr(), k.data_ptr(), v.data_ptr(), gates.data_ptr(), n, *sizes,
+                       obj.qkv_dtype, obj.gate_dtype, SOFTPLUS if softplus else 0)
         obj.step(q, k, v, gates, o, torch.cuda.current_stream())
-        _check("qmixer_step_output", lib().qmixer_step_output(
-            o.data_ptr(), rows[0], rows[1], _ptr(D), yp, ys, n, heads, d_v, code, st))
-    return y
+        _step_output(st, o.data_ptr(), rows[0], rows[1], dp, y.data_ptr(), _rows(fn, "out", y, 2), n, sizes[0],
+                     sizes[3], sizes[4])
+        return y
+    return _launch(fn, x, stream, body)
 
 
 # ---------------------------------------------------------------- norm
@@ -423,44 +446,51 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
     columns (a power of two from 8 to 256), or [.., 1] of whole rows for 0; a
     row or group without a finite maximum gets the scale NaN."""
     fn = "norm"
-    _tensor(fn, "x", x)
-    code = _code(fn, x)
-    if x.dim() < 1:
+    _tensor(fn, "x", x, None)
+    code, index, shape, xd = _code(fn, x), x.get_device(), x.shape, x.dtype
+    if len(shape) < 1:
         raise ValueError(f"{fn}: x must have rows")
-    columns = x.shape[-1]
-    _dense(fn, "weight", weight, x, x.dtype, (columns,))
+    columns = shape[-1]
+    wp = _dense(fn, "weight", weight, index, xd, (columns,))
     if residual is not None and gate is not None:
         raise ValueError(f"{fn}: residual or gate, not both")
-    if dtype not in _OUT:
+    kind = _OUT.get(dtype)
+    if kind is None:
         raise ValueError(f"{fn}: dtype {dtype} is not None, torch.int8 or torch.float8_e4m3fn")
-    if dtype is None and (group or scales is not None):
+    if kind == OUT_SAME and (group or scales is not None):
         raise ValueError(f"{fn}: group and scales go with 8-bit output")
     if group and (group < 0 or columns % group):
         raise ValueError(f"{fn}: groups of {group} do not divide {columns} columns")
-    other = residual if residual is not None else gate
-    shape = tuple(x.shape)
     x2 = _flat(fn, "x", x)
-    if other is not None:
-        _tensor(fn, "residual" if other is residual else "gate", other, x, x.dtype, shape)
-        o2 = _flat(fn, "residual" if other is residual else "gate", other)
-        if other is residual:
-            _overlap(fn, "residual", o2, "x", x2)
-    before = BEFORE_NONE if other is None else BEFORE_RESIDUAL if other is residual else BEFORE_GATE
-    rows = x2.shape[0]
-    with _On(x, stream) as st:
-        y = _out(fn, out, x, shape, dtype or x.dtype, (("x", x), ("residual or gate", other), ("weight", weight)))
+    before, name, other = ((BEFORE_RESIDUAL, "residual", residual) if residual is not None else
+                           (BEFORE_GATE, "gate", gate) if gate is not None else (BEFORE_NONE, None, None))
+    op, ostride = 0, 0
+    if before:
+        _tensor(fn, name, other, index, xd, shape)
+        o2 = _flat(fn, name, other)
+        op, ostride = o2.data_ptr(), _rows(fn, name, o2, 1)
+        if before == BEFORE_RESIDUAL:
+            _apart(fn, name, o2, "x", x2)
+            _apart(fn, name, o2, "weight", weight)
+    xs = _rows(fn, "x", x2, 1)
+
+    def body(st):
+        y = _out(fn, out, x, shape, dtype or xd, (("x", x), (name, other), ("weight", weight)))
         y2 = _flat(fn, "out", y)
-        if dtype is not None:
+        scale, sp = scales, 0
+        if kind:
             want = shape[:-1] + (columns // group if group else 1,)
-            if scales is None:
-                scales = torch.empty(want, dtype=torch.float32, device=x.device)
+            if scale is None:
+                scale = x.new_empty(want, dtype=_F32)
             else:
-                _dense(fn, "scales", scales, x, torch.float32, want)
-        _check("qmixer_norm", lib().qmixer_norm(
-            *_rows(fn, "x", x2, 1), *(_rows(fn, "residual or gate", o2, 1) if other is not None else (None, 0)),
-            weight.data_ptr(), *_rows(fn, "out", y2, 1), _ptr(scales), rows, columns, group, eps, code, before,
-            _OUT[dtype], st))
-    return y if dtype is None else (y, scales)
+                _dense(fn, "scales", scale, index, _F32, want)
+                for other_name, t in (("x", x2), (name, other), ("weight", weight), ("out", y2)):
+                    _apart(fn, "scales", scale, other_name, t)
+            sp = scale.data_ptr()
+        _norm(st, x2.data_ptr(), xs, op, ostride, wp, y2.data_ptr(), _rows(fn, "out", y2, 1), sp, x2.shape[0],
+              columns, group, eps, code, before, kind)
+        return (y, scale) if kind else y
+    return _launch(fn, x, stream, body)
 
 
 def _flat(fn, name, t):
@@ -468,6 +498,6 @@ def _flat(fn, name, t):
     if t.dim() == 2:
         return t
     try:
-        return t.view(-1, t.shape[-1]) if t.shape[-1] else t.reshape(-1, 0)
+        return t.view(-1, t.shape[-1]) if t.shape[-1] else t.reshape(0, 0)
     except RuntimeError:
         raise ValueError(f"{fn}: the rows of {name} must lie in one stride") from None

@@ -79,28 +79,63 @@ typedef enum { QMIXER_OUT_SAME = 0, QMIXER_OUT_INT8 = 1, QMIXER_OUT_E4M3 = 2 } q
 
 /* Causal convolution of width 2 to 4 over a prompt.  state may be NULL
  * without QMIXER_INITIAL (it is then not kept). */
-int qmixer_conv(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state,
-                void* y, int64_t y_stride, const int32_t* seq_starts, int32_t sequences,
-                int64_t tokens, int32_t channels, int32_t width, int32_t dtype, int32_t flags,
-                qstate_stream stream);
+typedef struct qmixer_conv_args {
+    const void* x;
+    int64_t x_stride;
+    const void* weight;
+    const void* bias;
+    void* state;
+    void* y;
+    int64_t y_stride;
+    const int32_t* seq_starts;
+    int32_t sequences;
+    int64_t tokens;
+    int32_t channels, width, dtype, flags;
+} qmixer_conv_args;
+int qmixer_conv(const qmixer_conv_args* args, qstate_stream stream);
 
 /* The same for one token of each sequence: x, y [batch][channels]; every row
  * of state moves on by one token. */
-int qmixer_conv_step(const void* x, int64_t x_stride, const void* weight, const void* bias,
-                     void* state, void* y, int64_t y_stride, int32_t batch, int32_t channels,
-                     int32_t width, int32_t dtype, int32_t flags, qstate_stream stream);
+typedef struct qmixer_conv_step_args {
+    const void* x;
+    int64_t x_stride;
+    const void* weight;
+    const void* bias;
+    void* state;
+    void* y;
+    int64_t y_stride;
+    int32_t batch, channels, width, dtype, flags;
+} qmixer_conv_step_args;
+int qmixer_conv_step(const qmixer_conv_step_args* args, qstate_stream stream);
 
 /* Selective scan of a prompt.  d_k and d_v 64 or 128, groups dividing heads.
  * dtype is the type of x, B, C and y, dt_dtype that of dt.  state may be NULL
  * without QMIXER_INITIAL.  workspace: qmixer_scan_workspace() bytes of device
  * memory on a 16-byte boundary, used by this call alone until it has run (two
  * graphs that may run at once need one each); QSTATE_EINVAL if it is smaller. */
-int qmixer_scan(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const float* A,
-                const void* B, int64_t B_stride, const void* C, int64_t C_stride, const float* D,
-                const float* dt_bias, float* state, void* y, int64_t y_stride,
-                const int32_t* seq_starts, int32_t sequences, int64_t tokens, int32_t heads,
-                int32_t groups, int32_t d_k, int32_t d_v, int32_t dtype, int32_t dt_dtype,
-                int32_t flags, void* workspace, int64_t workspace_bytes, qstate_stream stream);
+typedef struct qmixer_scan_args {
+    const void* x;
+    int64_t x_stride;
+    const void* dt;
+    int64_t dt_stride;
+    const float* A;
+    const void* B;
+    int64_t B_stride;
+    const void* C;
+    int64_t C_stride;
+    const float* D;
+    const float* dt_bias;
+    float* state;
+    void* y;
+    int64_t y_stride;
+    const int32_t* seq_starts;
+    int32_t sequences;
+    int64_t tokens;
+    int32_t heads, groups, d_k, d_v, dtype, dt_dtype, flags;
+    void* workspace;
+    int64_t workspace_bytes;
+} qmixer_scan_args;
+int qmixer_scan(const qmixer_scan_args* args, qstate_stream stream);
 
 /* Bytes of workspace that qmixer_scan needs for these sizes on the current
  * device; a negative return code for sizes that it refuses. */
@@ -109,28 +144,59 @@ int64_t qmixer_scan_workspace(int32_t sequences, int64_t tokens, int32_t heads, 
 
 /* The same for one token of each sequence on binary32 states: x, y
  * [batch][heads][d_v]; every state moves on by one token. */
-int qmixer_scan_step(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
-                     const float* A, const void* B, int64_t B_stride, const void* C,
-                     int64_t C_stride, const float* D, const float* dt_bias, float* state, void* y,
-                     int64_t y_stride, int32_t batch, int32_t heads, int32_t groups, int32_t d_k,
-                     int32_t d_v, int32_t dtype, int32_t dt_dtype, int32_t flags,
-                     qstate_stream stream);
+typedef struct qmixer_scan_step_args {
+    const void* x;
+    int64_t x_stride;
+    const void* dt;
+    int64_t dt_stride;
+    const float* A;
+    const void* B;
+    int64_t B_stride;
+    const void* C;
+    int64_t C_stride;
+    const float* D;
+    const float* dt_bias;
+    float* state;
+    void* y;
+    int64_t y_stride;
+    int32_t batch, heads, groups, d_k, d_v, dtype, dt_dtype, flags;
+} qmixer_scan_step_args;
+int qmixer_scan_step(const qmixer_scan_step_args* args, qstate_stream stream);
 
 /* One token of each sequence on a low-bit state: these operands, qstate_step
  * of a QSTATE_MAMBA2 object of one layer, then qmixer_step_output.  Writes
  * q = C and k = B of each head's group, v = dt x (qkv_dtype) and the gate
  * a = exp(dt A) (gate_dtype) in qstate_step's layouts. */
-int qmixer_step_operands(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
-                         const float* A, const void* B, int64_t B_stride, const void* C,
-                         int64_t C_stride, const float* dt_bias, void* q, void* k, void* v,
-                         void* gates, int32_t batch, int32_t heads, int32_t groups, int32_t d_k,
-                         int32_t d_v, int32_t dtype, int32_t dt_dtype, int32_t qkv_dtype,
-                         int32_t gate_dtype, int32_t flags, qstate_stream stream);
+typedef struct qmixer_step_operands_args {
+    const void* x;
+    int64_t x_stride;
+    const void* dt;
+    int64_t dt_stride;
+    const float* A;
+    const void* B;
+    int64_t B_stride;
+    const void* C;
+    int64_t C_stride;
+    const float* dt_bias;
+    void* q;
+    void* k;
+    void* v;
+    void* gates;
+    int32_t batch, heads, groups, d_k, d_v, dtype, dt_dtype, qkv_dtype, gate_dtype, flags;
+} qmixer_step_operands_args;
+int qmixer_step_operands(const qmixer_step_operands_args* args, qstate_stream stream);
 
 /* y = out + D x: out [batch][heads][d_v] binary32 as qstate_step leaves it. */
-int qmixer_step_output(const float* out, const void* x, int64_t x_stride, const float* D, void* y,
-                       int64_t y_stride, int32_t batch, int32_t heads, int32_t d_v, int32_t dtype,
-                       qstate_stream stream);
+typedef struct qmixer_step_output_args {
+    const float* out;
+    const void* x;
+    int64_t x_stride;
+    const float* D;
+    void* y;
+    int64_t y_stride;
+    int32_t batch, heads, d_v, dtype;
+} qmixer_step_output_args;
+int qmixer_step_output(const qmixer_step_output_args* args, qstate_stream stream);
 
 /* Root-mean-square norm.  before: QMIXER_BEFORE_RESIDUAL adds x to `other`
  * (the residual, which receives the sum in its own type) and normalises the
@@ -141,10 +207,21 @@ int qmixer_step_output(const float* out, const void* x, int64_t x_stride, const 
  * 448 (e4m3, rounded to nearest even); where max|y| is 0 the scale and codes
  * are 0, where it is not a finite number the scale is NaN and the codes 0.
  * columns 1 to 32768. */
-int qmixer_norm(const void* x, int64_t x_stride, void* other, int64_t other_stride,
-                const void* weight, void* y, int64_t y_stride, float* scales, int64_t rows,
-                int32_t columns, int32_t group, float eps, int32_t dtype, int32_t before,
-                int32_t out, qstate_stream stream);
+typedef struct qmixer_norm_args {
+    const void* x;
+    int64_t x_stride;
+    void* other;
+    int64_t other_stride;
+    const void* weight;
+    void* y;
+    int64_t y_stride;
+    float* scales;
+    int64_t rows;
+    int32_t columns, group;
+    float eps;
+    int32_t dtype, before, out;
+} qmixer_norm_args;
+int qmixer_norm(const qmixer_norm_args* args, qstate_stream stream);
 
 /* Quantise binary32 states S [rows][heads][d_k][d_v] (rows = layers * batch)
  * into codes and scales in qstate's layouts, ready for qstate_import: scale =
@@ -155,10 +232,17 @@ int qmixer_norm(const void* x, int64_t x_stride, void* other, int64_t other_stri
  * the yoked reference [rows][heads][d_k][d_v]) receives what is quantised.  A
  * group whose maximum is not a finite number gets unspecified codes; binary16
  * scales saturate at 65504 (neither is counted). */
-int qmixer_quantize(const float* S, void* codes, void* scales, float* ref, int64_t rows,
-                    int32_t heads, int32_t d_k, int32_t d_v, int32_t bits,
-                    const uint8_t* head_bits, int32_t group, int32_t scale_dtype, int32_t rotation,
-                    qstate_stream stream);
+typedef struct qmixer_quantize_args {
+    const float* S;
+    void* codes;
+    void* scales;
+    float* ref;
+    int64_t rows;
+    int32_t heads, d_k, d_v, bits;
+    const uint8_t* head_bits;
+    int32_t group, scale_dtype, rotation;
+} qmixer_quantize_args;
+int qmixer_quantize(const qmixer_quantize_args* args, qstate_stream stream);
 
 #ifdef __cplusplus
 }
