@@ -6,8 +6,7 @@
 // bit for bit.  Bound: memory (four bytes read, bits / 8 written an element).  A
 // CTA takes one tile and holds it in registers: a thread eight consecutive
 // columns at a time, so that one scale of a whole tile (group 0) costs no second
-// read.  Groups are joined by shuffles where they are a power of two of lanes,
-// else through shared memory.
+// read.  A group's lanes are joined by shuffles.
 #include "qmixer_common.cuh"
 
 namespace qm {
@@ -45,7 +44,7 @@ __device__ __forceinline__ int code_of(float x, float inv, float qmax) {
 template <int DK, int DV>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantParams p) {
     constexpr int kVecs = DK * DV / 8, kEach = kVecs / 256, kRow = DV / 8;
-    __shared__ uint32_t tops[kVecs];                // group maxima, or one per warp
+    __shared__ uint32_t tops[8];                    // the warps' maxima
     const int64_t tile = blockIdx.x;
     const int h = int(tile % p.heads);
     const int64_t row = tile / p.heads;
@@ -108,19 +107,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
         for (int w = 0; w < 8; w++) all = max(all, tops[w]);
 #pragma unroll
         for (int i = 0; i < kEach; i++) m[i] = all;
-    } else if ((lanes & (lanes - 1)) == 0) {
+    } else {
+        // a group divides d_v: a power of two of lanes
         for (int d = 1; d < lanes; d <<= 1)
 #pragma unroll
             for (int i = 0; i < kEach; i++) m[i] = max(m[i], __shfl_xor_sync(~0u, m[i], d));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kEach; i++) tops[i * 256 + threadIdx.x] = m[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const int u = i * 256 + threadIdx.x, first = u / kRow * kRow + u % kRow / lanes * lanes;
-            for (int j = 0; j < lanes; j++) m[i] = max(m[i], tops[first + j]);
-        }
     }
     const float qmax = (float)((1 << (bits - 1)) - 1);
     const int per_row = p.group ? DV / p.group : 1;
