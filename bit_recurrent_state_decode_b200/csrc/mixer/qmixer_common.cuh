@@ -51,12 +51,64 @@ __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
                                               pack_bf(v[4], v[5]), pack_bf(v[6], v[7]));
 }
 
-// z / (1 + e^-z).  The division's and the exponential's errors are a few units
-// of binary32, far inside the rounding of a bfloat16 result.
-__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-__device__ __forceinline__ float silu_full(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
-template <class T> __device__ __forceinline__ float silu(float z) {
-    return sizeof(T) == 2 ? silu_fast(z) : silu_full(z);
+// Two binary32 in one register pair: sm_100 issues an operation on both at once,
+// each half rounded as the scalar instruction rounds it.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 bf_pair(uint32_t u) { return pair(bf_lo(u), bf_hi(u)); }
+__device__ __forceinline__ uint32_t pack_bf(f2 v) {
+    const float2 f = unpair(v);
+    return pack_bf(f.x, f.y);
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// z / (1 + e^-z).  For bfloat16 results the hardware's exponential and reciprocal,
+// off by a few units of binary32: far inside the rounding that follows (and the
+// results that they flush to zero are below 2^-119).  Binary32 results take the
+// full functions.
+template <class T> __device__ __forceinline__ f2 silu2(f2 z) {
+    if constexpr (sizeof(T) == 2) {
+        const float2 t = unpair(mul2(z, pair(-1.44269504f, -1.44269504f)));
+        const float2 d = unpair(add2(pair(ex2_approx(t.x), ex2_approx(t.y)), pair(1.0f, 1.0f)));
+        return mul2(z, pair(rcp_approx(d.x), rcp_approx(d.y)));
+    } else {
+        const float2 v = unpair(z);
+        return pair(__fdiv_rn(v.x, 1.0f + expf(-v.x)), __fdiv_rn(v.y, 1.0f + expf(-v.y)));
+    }
 }
 
 // dt = softplus(z) = max(z, 0) + log(1 + e^-|z|): no overflow on either side.
@@ -87,8 +139,8 @@ struct Sequences {
 __device__ __forceinline__ int sequence_at(const Sequences& q, int64_t t) {
     if (!q.starts) {
         if (q.each == 0) return q.n - 1;
-        const int64_t i = t / q.each;
-        return i < q.n ? int(i) : q.n - 1;
+        const uint32_t i = (uint32_t)t / (uint32_t)q.each;      // tokens are below 2^31
+        return i < (uint32_t)q.n ? (int)i : q.n - 1;
     }
     int lo = 0, hi = q.n - 1;
     while (lo < hi) {

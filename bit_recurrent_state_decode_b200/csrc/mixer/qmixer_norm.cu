@@ -28,18 +28,52 @@ struct NormParams {
     int before, out;
 };
 
-template <class T, bool VEC>
-__device__ __forceinline__ void row8(const T* p, int left, float (&v)[8]) {
-    if constexpr (VEC) {
-        load8(p, v);
-    } else {
+
+__device__ __forceinline__ void floats(const f2 (&h)[4], float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = i < left ? to_f32<T>(p[i]) : 0.0f;
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpair(h[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
     }
 }
 
+// Eight elements as they lie in memory: all of a row's loads are issued before
+// the first is converted.
+template <class T, bool VEC> struct Eight;
+template <> struct Eight<bf16, true> {
+    uint4 r;
+    __device__ __forceinline__ void load(const bf16* p, int) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(f2 (&v)[4]) const {
+        v[0] = bf_pair(r.x); v[1] = bf_pair(r.y); v[2] = bf_pair(r.z); v[3] = bf_pair(r.w);
+    }
+};
+template <> struct Eight<float, true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p, int) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void get(f2 (&v)[4]) const {
+        v[0] = pair(a.x, a.y); v[1] = pair(a.z, a.w); v[2] = pair(b.x, b.y); v[3] = pair(b.z, b.w);
+    }
+};
+template <class T> struct Eight<T, false> {
+    float f[8];
+    __device__ __forceinline__ void load(const T* p, int left) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = i < left ? to_f32<T>(p[i]) : 0.0f;
+    }
+    __device__ __forceinline__ void get(f2 (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = pair(f[2 * i], f[2 * i + 1]);
+    }
+};
+
 template <class T, bool VEC>
-__device__ __forceinline__ void put8(T* p, int left, const float (&v)[8]) {
+__device__ __forceinline__ void put8(T* p, int left, const f2 (&h)[4]) {
+    float v[8];
+    floats(h, v);
     if constexpr (VEC) {
         store8(p, v);
     } else {
@@ -55,38 +89,59 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
+// The largest magnitude of eight, as bits.
+__device__ __forceinline__ uint32_t largest(const f2 (&h)[4]) {
+    float v[8];
+    floats(h, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+
 // The scale of a group from its largest magnitude (as bits: an integer maximum
 // keeps a NaN) and the codes of eight of its values.
 struct Codes {
     float scale, inv;
-    bool tiny;
+    bool odd;            // not a number, zero, or so small that its reciprocal may overflow
     __device__ __forceinline__ Codes(uint32_t most, float qmax) {
         const bool bad = most >= 0x7f800000u;
         scale = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(most), qmax);
-        inv = bad || scale == 0.0f ? 0.0f : __frcp_rn(scale);
-        tiny = scale < 1e-36f && scale > 0.0f;       // its reciprocal may overflow
-        if (tiny) inv = 0.0f;
-        if (bad) inv = __uint_as_float(0x7fc00000u);
+        odd = !(scale >= 1e-36f);
+        inv = __frcp_rn(scale);
     }
-    __device__ __forceinline__ float at(float y) const {
-        return tiny ? __fdiv_rn(y, scale) : inv != inv ? 0.0f : y * inv;
+    __device__ __forceinline__ void divide(const f2 (&y)[4], float (&z)[8]) const {
+        f2 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) q[i] = mul2(y[i], pair(inv, inv));
+        floats(q, z);
+        if (odd) {
+            float v[8];
+            floats(y, v);
+#pragma unroll
+            for (int i = 0; i < 8; i++) z[i] = scale > 0.0f ? __fdiv_rn(v[i], scale) : 0.0f;
+        }
     }
-    __device__ __forceinline__ uint2 int8(const float (&y)[8]) const {
+    __device__ __forceinline__ uint2 int8(const f2 (&y)[4]) const {
+        float z[8];
         uint32_t c[8];
+        divide(y, z);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const float q = fminf(fmaxf(at(y[i]), -127.0f), 127.0f);
-            c[i] = __float_as_uint(q + 12582912.0f) & 0xffu;      // 1.5 * 2^23: rounds half to even
+            const float q = fminf(fmaxf(z[i], -127.0f), 127.0f);
+            c[i] = __float_as_uint(q + 12582912.0f);              // 1.5 * 2^23: rounds half to even
         }
-        return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+        return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x40), __byte_perm(c[2], c[3], 0x40), 0x5410),
+                          __byte_perm(__byte_perm(c[4], c[5], 0x40), __byte_perm(c[6], c[7], 0x40), 0x5410));
     }
-    __device__ __forceinline__ uint2 e4m3(const float (&y)[8]) const {
-        return make_uint2(e4m3x2(at(y[0]), at(y[1])) | e4m3x2(at(y[2]), at(y[3])) << 16,
-                          e4m3x2(at(y[4]), at(y[5])) | e4m3x2(at(y[6]), at(y[7])) << 16);
+    __device__ __forceinline__ uint2 e4m3(const f2 (&y)[4]) const {
+        float z[8];
+        divide(y, z);
+        return make_uint2(e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16, e4m3x2(z[4], z[5]) | e4m3x2(z[6], z[7]) << 16);
     }
 };
 
-template <class T, bool VEC, int THREADS, int N>
+template <class T, bool VEC, int BEFORE, int THREADS, int N>
 __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(const NormParams p) {
     constexpr int kBlock = THREADS < 128 ? 128 : THREADS;
     constexpr int kWarps = THREADS / 32;
@@ -99,37 +154,40 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
     T* const other = static_cast<T*>(p.other) + row * p.os;
     const T* const w = static_cast<const T*>(p.w);
 
-    float h[N][8];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int c = (i * THREADS + tid) * 8, left = p.columns - c;
-        if (left > 0) row8<T, VEC>(x + c, left, h[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; j++) h[i][j] = 0.0f;
-    }
-    if (p.before != QMIXER_BEFORE_NONE) {
+    f2 h[N][4];
+    {
+        Eight<T, VEC> xr[N], orow[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+            if (left > 0) {
+                xr[i].load(x + c, left);
+                if (BEFORE != QMIXER_BEFORE_NONE) orow[i].load(other + c, left);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int c = (i * THREADS + tid) * 8, left = p.columns - c;
+#pragma unroll
+            for (int j = 0; j < 4; j++) h[i][j] = 0;
             if (left <= 0) continue;
-            float o[8];
-            row8<T, VEC>(other + c, left, o);
-            if (p.before == QMIXER_BEFORE_RESIDUAL) {
+            xr[i].get(h[i]);
+            if constexpr (BEFORE != QMIXER_BEFORE_NONE) {
+                f2 o[4];
+                orow[i].get(o);
 #pragma unroll
-                for (int j = 0; j < 8; j++) h[i][j] += o[j];
-                put8<T, VEC>(other + c, left, h[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; j++) h[i][j] *= silu<T>(o[j]);
+                for (int j = 0; j < 4; j++)
+                    h[i][j] = BEFORE == QMIXER_BEFORE_RESIDUAL ? add2(h[i][j], o[j]) : mul2(h[i][j], silu2<T>(o[j]));
+                if (BEFORE == QMIXER_BEFORE_RESIDUAL) put8<T, VEC>(other + c, left, h[i]);
             }
         }
     }
+    f2 squares = 0;
 #pragma unroll
     for (int i = 0; i < N; i++)
 #pragma unroll
-        for (int j = 0; j < 8; j++) sum = fmaf(h[i][j], h[i][j], sum);
+        for (int j = 0; j < 4; j++) squares = fma2(h[i][j], h[i][j], squares);
+    float sum = unpair(squares).x + unpair(squares).y;
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
     if constexpr (THREADS > 32) {
@@ -145,13 +203,13 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
     for (int i = 0; i < N; i++) {
         const int c = (i * THREADS + tid) * 8, left = p.columns - c;
         if (left <= 0) continue;
-        float g[8];
-        row8<T, VEC>(w + c, left, g);
+        f2 g[4];
+        Eight<T, VEC> wr;
+        wr.load(w + c, left);
+        wr.get(g);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            h[i][j] = h[i][j] * r * g[j];
-            if (VEC || j < left) most = max(most, __float_as_uint(h[i][j]) & 0x7fffffffu);
-        }
+        for (int j = 0; j < 4; j++) h[i][j] = mul2(mul2(h[i][j], pair(r, r)), g[j]);
+        if (p.out != QMIXER_OUT_SAME && !p.group) most = max(most, largest(h[i]));
     }
     if (p.out == QMIXER_OUT_SAME) {
         T* const y = static_cast<T*>(p.y) + row * p.ys;
@@ -179,10 +237,7 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
         const int c = (i * THREADS + tid) * 8, left = p.columns - c;
         uint32_t m = most;
         if (p.group) {
-            m = 0;
-            if (left > 0)
-#pragma unroll
-                for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(h[i][j]) & 0x7fffffffu);
+            m = left > 0 ? largest(h[i]) : 0;
             for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
         }
         if (left <= 0) continue;
@@ -200,27 +255,32 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
     }
 }
 
-template <class T, bool VEC, int THREADS, int N> void launch_norm(const NormParams& p, cudaStream_t st) {
+template <class T, bool VEC, int BEFORE, int THREADS, int N> void launch_norm(const NormParams& p, cudaStream_t st) {
     constexpr int kBlock = THREADS < 128 ? 128 : THREADS;
     const int64_t per = kBlock / THREADS;
-    norm_kernel<T, VEC, THREADS, N><<<(unsigned)((p.rows + per - 1) / per), kBlock, 0, st>>>(p);
+    norm_kernel<T, VEC, BEFORE, THREADS, N><<<(unsigned)((p.rows + per - 1) / per), kBlock, 0, st>>>(p);
 }
 
-// A row of up to 32 * 8 * N columns in one warp, N = 1, 2, 4, 8; wider ones, or
-// few rows, in 128 or 512 threads.
-template <class T, bool VEC> void dispatch_norm(const NormParams& p, cudaStream_t st) {
+// Up to 1024 columns in a warp of its own where there are rows enough to fill the
+// SMs, else 128 threads a row; beyond 4096 columns 512.
+template <class T, bool VEC, int BEFORE> void by_columns(const NormParams& p, cudaStream_t st) {
     const int v = (p.columns + 7) / 8;
     const bool few = p.rows < 148 * 8;
-    if (v <= 32) launch_norm<T, VEC, 32, 1>(p, st);
-    else if (!few && v <= 64) launch_norm<T, VEC, 32, 2>(p, st);
-    else if (!few && v <= 128) launch_norm<T, VEC, 32, 4>(p, st);
-    else if (!few && v <= 256) launch_norm<T, VEC, 32, 8>(p, st);
-    else if (v <= 128) launch_norm<T, VEC, 128, 1>(p, st);
-    else if (v <= 256) launch_norm<T, VEC, 128, 2>(p, st);
-    else if (v <= 512) launch_norm<T, VEC, 128, 4>(p, st);
-    else if (v <= 1024) launch_norm<T, VEC, 512, 2>(p, st);
-    else if (v <= 2048) launch_norm<T, VEC, 512, 4>(p, st);
-    else launch_norm<T, VEC, 512, 8>(p, st);
+    if (v <= 32) launch_norm<T, VEC, BEFORE, 32, 1>(p, st);
+    else if (!few && v <= 64) launch_norm<T, VEC, BEFORE, 32, 2>(p, st);
+    else if (!few && v <= 128) launch_norm<T, VEC, BEFORE, 32, 4>(p, st);
+    else if (v <= 128) launch_norm<T, VEC, BEFORE, 128, 1>(p, st);
+    else if (v <= 256) launch_norm<T, VEC, BEFORE, 128, 2>(p, st);
+    else if (v <= 512) launch_norm<T, VEC, BEFORE, 128, 4>(p, st);
+    else if (v <= 1024) launch_norm<T, VEC, BEFORE, 512, 2>(p, st);
+    else if (v <= 2048) launch_norm<T, VEC, BEFORE, 512, 4>(p, st);
+    else launch_norm<T, VEC, BEFORE, 512, 8>(p, st);
+}
+
+template <class T, bool VEC> void dispatch_norm(const NormParams& p, cudaStream_t st) {
+    if (p.before == QMIXER_BEFORE_NONE) by_columns<T, VEC, QMIXER_BEFORE_NONE>(p, st);
+    else if (p.before == QMIXER_BEFORE_RESIDUAL) by_columns<T, VEC, QMIXER_BEFORE_RESIDUAL>(p, st);
+    else by_columns<T, VEC, QMIXER_BEFORE_GATE>(p, st);
 }
 
 }  // namespace qm
