@@ -80,7 +80,9 @@ _conv, _conv_step, _scan, _scan_step, _step_operands, _step_output, _norm, _quan
 # ---------------------------------------------------------------- argument checks
 _CODE = {torch.float32: Q.F32, torch.bfloat16: Q.BF16}
 _F32 = torch.float32
-# address of a device's current stream (torch.cuda.current_stream builds an object first)
+# the current device and the address of its current stream (a tensor was seen, so
+# CUDA is initialised; torch.cuda's own calls check that and build an object first)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -162,7 +164,7 @@ def _launch(fn, t, stream, body):
     """body(address of the stream) with the tensors' device current, and, on a
     stream of the caller's, its allocations belonging to that stream."""
     index = t.get_device()
-    if stream is None and index == torch.cuda.current_device():
+    if stream is None and index == _current_device():
         return body(_raw_stream(index))
     if stream is not None and stream.device.index != index:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {t.device}")
@@ -187,11 +189,14 @@ def _sequences(fn, lead, seq_starts, index):
     return seq_starts.numel() - 1, lead[0], seq_starts.data_ptr()
 
 
-def _out(fn, out, like, shape, dtype, inputs):
-    if out is None:
-        if dtype is like.dtype and like.is_contiguous():
-            return torch.empty_like(like)
-        return like.new_empty(shape, dtype=dtype)
+def _fresh(like, shape, dtype):
+    if dtype is like.dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _given(fn, out, like, shape, dtype, inputs):
+    """The caller's `out`, apart from the inputs."""
     _tensor(fn, "out", out, like.get_device(), dtype, shape)
     for name, t in inputs:
         _apart(fn, "out", out, name, t)
@@ -222,8 +227,12 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
     xs = _rows(fn, "x", x, 1)
 
     def body(st):
-        y = _out(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
-        _conv(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), _rows(fn, "out", y, 1), starts, n, tokens, shape[-1],
+        if out is None:
+            y, ys = _fresh(x, shape, x.dtype), shape[-1]
+        else:
+            y = _given(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
+            ys = _rows(fn, "out", y, 1)
+        _conv(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), ys, starts, n, tokens, shape[-1],
               width, code, (INITIAL if initial else 0) | (SILU if activation else 0))
         return y
     return _launch(fn, x, stream, body)
@@ -243,8 +252,12 @@ def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=
     xs = _rows(fn, "x", x, 1)
 
     def body(st):
-        y = _out(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
-        _conv_step(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), _rows(fn, "out", y, 1), shape[0], shape[1], width,
+        if out is None:
+            y, ys = _fresh(x, shape, x.dtype), shape[1]
+        else:
+            y = _given(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
+            ys = _rows(fn, "out", y, 1)
+        _conv_step(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), ys, shape[0], shape[1], width,
                    code, SILU if activation else 0)
         return y
     return _launch(fn, x, stream, body)
@@ -260,8 +273,8 @@ def _taps(fn, x, weight, bias, state, n, index):
     sp = 0
     if state is not None:
         sp = _dense(fn, "state", state, index, dtype, (n, width - 1, channels))
-        end, at = sp + state.nbytes, x.data_ptr()
-        if at < end and sp < at + _span(x):
+        at = x.data_ptr()       # by bounds first
+        if at < sp + state.nbytes and sp < at + x.shape[0] * x.stride(0) * 4:
             _apart(fn, "state", state, "x", x)
     return width, weight.data_ptr(), bp, sp
 
@@ -337,10 +350,14 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
         _states_apart(fn, state, sp, rows, x, dt, B, C)
 
     def body(st):
-        y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
+        if out is None:
+            y, ys = _fresh(x, x.shape, x.dtype), sizes[0] * sizes[3]
+        else:
+            y = _given(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
+            ys = _rows(fn, "out", y, 2)
         size = _workspace(index, n, tokens, *sizes[:5])
         work = x.new_empty(size, dtype=torch.uint8) if size else None
-        _scan(st, *rows, dp, biasp, sp, y.data_ptr(), _rows(fn, "out", y, 2), starts, n, tokens, *sizes,
+        _scan(st, *rows, dp, biasp, sp, y.data_ptr(), ys, starts, n, tokens, *sizes,
               (INITIAL if initial else 0) | (SOFTPLUS if softplus else 0), work.data_ptr() if size else 0, size)
         return y
     return _launch(fn, x, stream, body)
@@ -359,8 +376,12 @@ def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out
     _states_apart(fn, state, sp, rows, x, dt, B, C)
 
     def body(st):
-        y = _out(fn, out, x, shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
-        _scan_step(st, *rows, dp, biasp, sp, y.data_ptr(), _rows(fn, "out", y, 2), n, *sizes,
+        if out is None:
+            y, ys = _fresh(x, shape, x.dtype), sizes[0] * sizes[3]
+        else:
+            y = _given(fn, out, x, shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
+            ys = _rows(fn, "out", y, 2)
+        _scan_step(st, *rows, dp, biasp, sp, y.data_ptr(), ys, n, *sizes,
                    SOFTPLUS if softplus else 0)
         return y
     return _launch(fn, x, stream, body)
@@ -419,14 +440,18 @@ def step(obj, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, out=None, 
         raise ValueError(f"{fn}: x is on {x.device}, the object on cuda:{obj.device}")
 
     def body(st):
-        y = _out(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt)))
+        if out is None:
+            y, ys = _fresh(x, x.shape, x.dtype), sizes[0] * sizes[3]
+        else:
+            y = _given(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt)))
+            ys = _rows(fn, "out", y, 2)
         if n == 0:
             return y
         q, k, v, gates, o = obj.alloc_inputs(x.device)
         _step_operands(st, *rows, biasp, q.data_ptr(), k.data_ptr(), v.data_ptr(), gates.data_ptr(), n, *sizes,
                        obj.qkv_dtype, obj.gate_dtype, SOFTPLUS if softplus else 0)
         obj.step(q, k, v, gates, o, torch.cuda.current_stream())
-        _step_output(st, o.data_ptr(), rows[0], rows[1], dp, y.data_ptr(), _rows(fn, "out", y, 2), n, sizes[0],
+        _step_output(st, o.data_ptr(), rows[0], rows[1], dp, y.data_ptr(), ys, n, sizes[0],
                      sizes[3], sizes[4])
         return y
     return _launch(fn, x, stream, body)
@@ -470,13 +495,21 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
         o2 = _flat(fn, name, other)
         op, ostride = o2.data_ptr(), _rows(fn, name, o2, 1)
         if before == BEFORE_RESIDUAL:
-            _apart(fn, name, o2, "x", x2)
-            _apart(fn, name, o2, "weight", weight)
+            at, end = x2.data_ptr(), x2.shape[0] * x2.stride(0) * 4      # by bounds first
+            if at < op + o2.shape[0] * ostride * 4 and op < at + end:
+                _apart(fn, name, o2, "x", x2)
+            if wp < op + o2.shape[0] * ostride * 4 and op < wp + weight.nbytes:
+                _apart(fn, name, o2, "weight", weight)
     xs = _rows(fn, "x", x2, 1)
 
     def body(st):
-        y = _out(fn, out, x, shape, dtype or xd, (("x", x), (name, other), ("weight", weight)))
-        y2 = _flat(fn, "out", y)
+        if out is None:
+            y = y2 = _fresh(x, shape, dtype or xd)
+            ys = columns
+        else:
+            y = _given(fn, out, x, shape, dtype or xd, (("x", x), (name, other), ("weight", weight)))
+            y2 = _flat(fn, "out", y)
+            ys = _rows(fn, "out", y2, 1)
         scale, sp = scales, 0
         if kind:
             want = shape[:-1] + (columns // group if group else 1,)
@@ -487,7 +520,7 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
                 for other_name, t in (("x", x2), (name, other), ("weight", weight), ("out", y2)):
                     _apart(fn, "scales", scale, other_name, t)
             sp = scale.data_ptr()
-        _norm(st, x2.data_ptr(), xs, op, ostride, wp, y2.data_ptr(), _rows(fn, "out", y2, 1), sp, x2.shape[0],
+        _norm(st, x2.data_ptr(), xs, op, ostride, wp, y2.data_ptr(), ys, sp, x2.shape[0],
               columns, group, eps, code, before, kind)
         return (y, scale) if kind else y
     return _launch(fn, x, stream, body)
