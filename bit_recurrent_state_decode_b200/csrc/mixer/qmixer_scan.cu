@@ -69,7 +69,8 @@ int sm_count() {
 // on top.
 ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, int dtype, bool ragged, int sms) {
     const int64_t unit = dtype == QSTATE_BF16 ? kChunk : kBatchTokens;
-    const int64_t chains = (int64_t)heads * (dv / 64), resident = 2 * sms;
+    // CTAs that an SM holds: two of the recurrent form, one of the chunked
+    const int64_t chains = (int64_t)heads * (dv / 64), resident = (dtype == QSTATE_BF16 ? 1 : 2) * sms;
     const int64_t mean = tokens / sequences, longest = ragged ? (4 * mean < tokens ? 4 * mean : tokens) : mean;
     const int64_t even = tokens * chains / resident;
     ScanPlan o{};

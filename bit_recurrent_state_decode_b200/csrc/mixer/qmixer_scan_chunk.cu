@@ -20,13 +20,24 @@
 // is binary32 and carried on: it is split into three bfloat16 terms, 24 bits.
 // The state itself lives in binary32 registers.
 //
-// Work.  A CTA of eight warps takes 64 value columns of one head over one
-// segment; two CTAs share an SM, so that one computes while the other waits for
-// its loads or products.  Tensor memory, 256 columns a CTA: G (128), later Y and
-// the state's increment; C S (64); M (64, as the A operand of M X).  Shared
-// memory: C, B, X as TMA lays them down (128-byte swizzle), S.  w X takes C's and
-// S's places once G and C S are done.  B serves twice, by rows for G and by
-// columns (transposed descriptor) for B^T.
+// Work.  A CTA takes 64 value columns of one head over one segment and fills an
+// SM.  Only S chains one chunk to the next, so its warps have roles that run a
+// chunk ahead of each other and meet at mbarriers:
+//   load     C, B, X of two chunks by TMA (128-byte swizzle)
+//   product  two warps: C S and the increment B^T (w X), which the next chunk waits
+//            for, and G and M X, which no chunk waits for
+//   M        eight warps: the decays two chunks ahead; G from tensor memory, M back
+//            to it (as the A operand)
+//   W        eight warps: w X in three parts to shared memory
+//   E        eight warps: S, half a row a thread in registers, from the increment,
+//            its bfloat16 copy to shared memory; then y
+// Tensor memory: G (128 columns), C S (2 x 64), M X (64), M (64), the increment (128:
+// the first two parts of w X are one product of 128 columns, for reading B^T from
+// shared memory bounds it).  Shared memory: two stages of C, B, X, two parts of w X,
+// and one place that holds S, then, once C S is done, the third part.  B serves
+// twice, by rows for G and by columns (transposed descriptor) for B^T.  Loops are
+// unrolled no further than they have to be: the roles share the instruction cache,
+// and with all of it unrolled a chunk took twice as long.
 #include <cuda.h>
 
 #include "qmixer_scan.cuh"
@@ -42,6 +53,15 @@ __device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
 }
 __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_at(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_at(b)), "r"(parity)
+        : "memory");
+    return ok;
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
     for (uint32_t i = 0; i < kPolls; i++) {
@@ -62,12 +82,17 @@ __device__ __forceinline__ void tma_load(void* to, const CUtensorMap* map, int x
         "l"(map), "r"(x), "r"(y), "r"(smem_at(b))
         : "memory");
 }
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint64_t* b) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_at(b))
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_at(b))
+        : "memory");
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start, the stride between
@@ -82,41 +107,63 @@ __host__ __device__ constexpr uint32_t ins(int n, bool a_by_columns, bool b_by_c
     return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_by_columns << 15 | (uint32_t)b_by_columns << 16 |
            (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
+// Called by a whole warp, so that the descriptors stay in uniform registers; one
+// elected lane issues.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
-__device__ __forceinline__ void tm_load32(uint32_t at, float (&v)[32]) {
-    uint32_t r[32];
+// Sixteen columns at two places, on their way together.
+__device__ __forceinline__ void tm_load16(uint32_t at, uint32_t at2, float (&v)[16], float (&w)[16]) {
+    uint32_t r[16], q[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(at),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%32];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%33];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+          "=&r"(q[0]), "=&r"(q[1]), "=&r"(q[2]), "=&r"(q[3]), "=&r"(q[4]), "=&r"(q[5]), "=&r"(q[6]), "=&r"(q[7]),
+          "=&r"(q[8]), "=&r"(q[9]), "=&r"(q[10]), "=&r"(q[11]), "=&r"(q[12]), "=&r"(q[13]), "=&r"(q[14]), "=&r"(q[15])
+        : "r"(at), "r"(at2)
         : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        v[i] = __uint_as_float(r[i]);
+        w[i] = __uint_as_float(q[i]);
+    }
+}
+__device__ __forceinline__ void tm_load8(uint32_t at, uint32_t at2, float (&v)[8], float (&w)[8]) {
+    uint32_t r[8], q[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+          "=&r"(q[0]), "=&r"(q[1]), "=&r"(q[2]), "=&r"(q[3]), "=&r"(q[4]), "=&r"(q[5]), "=&r"(q[6]), "=&r"(q[7])
+        : "r"(at), "r"(at2)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        v[i] = __uint_as_float(r[i]);
+        w[i] = __uint_as_float(q[i]);
+    }
+}
+__device__ __forceinline__ void tm_store8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // ------------------------------------------------------------ shared memory
@@ -130,46 +177,89 @@ struct Scalars {
 
 template <int N, bool OUT> struct ChunkSmem {
     static constexpr int kOp = N * kChunk * 2;               // bytes of B or C
-    static constexpr int kX = 64 * kChunk * 2;
-    // offsets in the 1024-byte aligned part.  w X: three parts of kX.
-    static constexpr int kB = 0, kXs = kB + kOp, kC = kXs + kX;
-    static constexpr int kW0 = kC, kW1 = kC + kX;            // in C's place (N = 128) or behind it
-    static constexpr int kS = kC + 2 * kX, kW2 = kS;
-    static constexpr int kEnd = kS + kX;
-    static constexpr int kBytes = kEnd + 1024 + 2 * (int)sizeof(Scalars) + 64 * 4 + 64;
+    static constexpr int kX = 64 * kChunk * 2;               // bytes of X, of a part of w X, room of S
+    // offsets in the 1024-byte aligned part; a stage is B, X, C.  (The products
+    // read 128 columns of B by columns: for N = 64 the second half is X, and rows
+    // of tensor memory that nothing reads.)
+    static constexpr int kB = 0, kXs = kOp, kC = kOp + kX;
+    static constexpr int kStage = kOp + kX + (OUT ? kOp : 0);
+    static constexpr int kW0 = 2 * kStage, kW1 = kW0 + kX, kW2 = kW1 + kX, kS = kW2;
+    static constexpr int kEnd = kW2 + kX;
+    static constexpr int kBytes = kEnd + 1024 + 3 * (int)sizeof(Scalars) + 2 * 64 * 4 + 22 * 8 + 16;
 };
+static_assert(ChunkSmem<128, true>::kBytes <= 232448, "shared memory of a CTA");
+
+// mbarriers.  No waiter may fall two phases behind; those with more places take turns
+// by chunk (three: by threes), where a phase may end before all have waited for the
+// one in front of it.
+enum { B_FULL = 0, B_SC = 2, B_E = 5, B_W01 = 7, B_G = 9, B_D = 11, B_Y = 13, B_YO, B_W2, B_M, B_S, B_WSYNC, B_DRAIN, kBars = B_DRAIN + 2 };
 
 // Byte offset of 16-byte piece c of row r in rows of 128 bytes, swizzled.
 __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(b)) : "memory");
+}
+// One arrival of a warp whose lanes are done (their own fences come before).
+__device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(b);
+}
+__device__ __forceinline__ void store32(bf16* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// warps 0 to 7: E, 8 to 15: M, 16 to 23: W, 24 and 25: products, 26: load
+constexpr int kThreads = 864;
+constexpr uint32_t kG = 0, kYo = 128, kY = 256, kM = 320, kD = 384;      // tensor memory columns
+
 template <int N, bool OUT>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUtensorMap mx,
              const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc) {
     using L = ChunkSmem<N, OUT>;
     extern __shared__ unsigned char raw[];
     unsigned char* const sm = raw + ((1024 - (smem_at(raw) & 1023)) & 1023);
     Scalars* const scal = reinterpret_cast<Scalars*>(sm + L::kEnd);
-    int* const bad = reinterpret_cast<int*>(scal + 2);            // first non-finite token of a column
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(bad + 64);  // loads, products a, products b
-    uint32_t* const tm_slot = reinterpret_cast<uint32_t*>(bars + 3);
-    constexpr uint32_t kTmem = OUT ? 256 : 64;
-    constexpr uint32_t kG = 0, kD = 0, kY = 64, kYo = 128, kM = 192;
+    int* const bad = reinterpret_cast<int*>(scal + 3);            // [2][64]: a column's first non-finite token, by chunk
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(bad + 128);
+    uint32_t* const tm_slot = reinterpret_cast<uint32_t*>(bars + 22);
+    static_assert(kBars <= 22, "room");
+    constexpr uint32_t kTmem = 512;
 
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, quad = warp & 3, half = warp >> 2;
+    // the same in all lanes, and known to be: only then do the products' descriptors
+    // live in uniform registers (else each product takes 135 cycles to issue, not 48)
+    auto uniform = [](uint32_t v) { return __shfl_sync(~0u, v, 0); };
+    const int tid = threadIdx.x, warp = (int)uniform(tid / 32), lane = tid & 31, quad = warp & 3;
     Segment seg;
     if (!find_segment(p, blockIdx.x, seg)) return;
     if (!OUT && seg.last) return;
     const int parts = p.dv / 64, h = blockIdx.y / parts, c0 = blockIdx.y % parts * 64, g = h / p.per_group;
-    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, D = OUT && p.D ? p.D[h] : 0.0f;
+    // (seg.to may lie below seg.from)
+    const int chunks = (int)uniform((uint32_t)(seg.to > seg.from ? (seg.to - seg.from + kChunk - 1) / kChunk : 0));
 
     if (tid == 0) {
-#pragma unroll
-        for (int i = 0; i < 3; i++) bar_init(bars + i, 1);
+        for (int i = 0; i < 2; i++) {
+            bar_init(bars + B_FULL + i, 2);
+            bar_init(bars + B_G + i, 1);
+            bar_init(bars + B_D + i, 1);
+            bar_init(bars + B_E + i, 8);
+            bar_init(bars + B_W01 + i, 8);
+            bar_init(bars + B_DRAIN + i, 1);
+        }
+        bar_init(bars + B_YO, 1);
+        bar_init(bars + B_W2, 8);
+        bar_init(bars + B_M, 8);
+        bar_init(bars + B_S, 8);
+        bar_init(bars + B_WSYNC, 8);
+        for (int i = 0; i < 3; i++) bar_init(bars + B_SC + i, 4);
+        bar_init(bars + B_Y, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
-    if (tid < 64) bad[tid] = kChunk;
+    if (tid < 128) bad[tid] = kChunk;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(tm_slot)),
                      "r"(kTmem)
@@ -177,292 +267,431 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     __syncthreads();
-    const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(tm_slot);
+    const uint32_t tm = uniform(*reinterpret_cast<volatile uint32_t*>(tm_slot));
     const uint32_t tq = tm + ((uint32_t)(quad * 32) << 16);
-
-    // the state: row n, columns half * 32 ..
-    const int row = quad * 32 + lane;
-    const bool holds = row < N;
-    float S[32];
-    {
-        const float* from = nullptr;
-        if (OUT && p.cut) from = p.seg_state + ((int64_t)blockIdx.x * p.heads + h) * N * p.dv;
-        else if (OUT && p.initial) from = p.state + ((int64_t)seg.sequence * p.heads + h) * N * p.dv;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float4 v = make_float4(0, 0, 0, 0);
-            if (from && holds) v = *reinterpret_cast<const float4*>(from + (int64_t)row * p.dv + c0 + half * 32 + i);
-            S[i] = v.x; S[i + 1] = v.y; S[i + 2] = v.z; S[i + 3] = v.w;
-        }
-    }
-    auto put_state = [&] {
-        if (OUT && holds) {
-#pragma unroll
-            for (int c = 0; c < 4; c++)
-                *reinterpret_cast<uint4*>(sm + L::kS + swz(row, half * 4 + c)) =
-                    make_uint4(pack_bf(S[c * 8], S[c * 8 + 1]), pack_bf(S[c * 8 + 2], S[c * 8 + 3]),
-                               pack_bf(S[c * 8 + 4], S[c * 8 + 5]), pack_bf(S[c * 8 + 6], S[c * 8 + 7]));
-        }
-        fence_async();
-    };
-    auto load = [&](int64_t t0) {           // thread 0
-        const int t = (int)t0;
-        bar_expect(bars, (OUT ? 2 : 1) * L::kOp + L::kX);
-#pragma unroll
-        for (int i = 0; i < N / 64; i++) {
-            tma_load(sm + L::kB + i * 16384, &mb, g * N + i * 64, t, bars);
-            if (OUT) tma_load(sm + L::kC + i * 16384, &mc, g * N + i * 64, t, bars);
-        }
-        tma_load(sm + L::kXs, &mx, h * p.dv + c0, t, bars);
-    };
-    float raw_dt = 0.0f;
-    auto fetch_dt = [&](int64_t t0) {       // threads below 128
-        raw_dt = tid < kChunk && t0 + tid < seg.to ? load_dt(p.dt, (t0 + tid) * p.dts + h, p.dt_bf16) : 0.0f;
-    };
-    auto scalars = [&](int64_t t0, Scalars& s) {
-        if (tid >= kChunk) return;
-        const bool in = t0 + tid < seg.to;
-        const float dt = in ? time_step(raw_dt, bias, p.softplus) : 0.0f, a = in ? expf(dt * A) : 1.0f;
-        float up = a, down = a;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const float u = __shfl_up_sync(~0u, up, d), v = __shfl_down_sync(~0u, down, d);
-            if (lane >= d) up *= u;
-            if (lane + d < 32) down *= v;
-        }
-        float behind = __shfl_down_sync(~0u, down, 1);
-        if (lane == 31) behind = 1.0f;
-        s.a[tid] = a;
-        s.dt[tid] = dt;
-        s.upto[tid] = up;
-        s.behind[tid] = behind * dt;
-        if (lane == 31) s.block[warp] = up;
-    };
-
     bool ok = true;
-    float total = 1.0f;
-    int64_t t0 = seg.from;
-    if (t0 < seg.to) {
-        if (tid == 0) load(t0);
-        fetch_dt(t0);
-        scalars(t0, scal[0]);
-        put_state();
-        if (t0 + kChunk < seg.to) fetch_dt(t0 + kChunk);
-    }
-    for (uint32_t it = 0; t0 < seg.to; t0 += kChunk, it++) {
-        const uint32_t par = it & 1;
-        const Scalars& sc = scal[par];
-        const int valid = seg.to - t0 < kChunk ? (int)(seg.to - t0) : kChunk;
-        ok = bar_wait(bars, par);
-        if (valid < kChunk) {
-            // rows of other sequences or of nothing: zero, whatever they hold
-            for (int i = tid; i < (kChunk - valid) * (N / 8 + 8); i += 256) {
-                const int r = valid + i / (N / 8 + 8), c = i % (N / 8 + 8);
-                unsigned char* at = c < N / 8 ? sm + L::kB + c / 8 * 16384 + r * 128 + c % 8 * 16
-                                              : sm + L::kXs + r * 128 + (c - N / 8) * 16;
-                *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+    // wait for phase `k` of a barrier, or for chunk c's of two or three that take turns
+    // (lanes of a warp may differ in when they give up: all do when one does)
+    auto wait = [&](int b, int k) { return ok = ok && __all_sync(~0u, bar_wait(bars + b, k & 1)); };
+    auto wait2 = [&](int b, int c) { return ok = ok && __all_sync(~0u, bar_wait(bars + b + (c & 1), (c >> 1) & 1)); };
+
+    auto wait3 = [&](int b, int c) { return ok = ok && __all_sync(~0u, bar_wait(bars + b + c % 3, c / 3 & 1)); };
+
+    if (warp == 26) {
+        // ---------------------------------------------------- load
+        int issued = 0, half = 0;
+        for (int c = 0; c < chunks; c++) {
+            unsigned char* const st = sm + (c & 1) * L::kStage;
+            uint64_t* const full = bars + B_FULL + (c & 1);
+            const int t = (int)(seg.from + (int64_t)c * kChunk);
+            // B and C as soon as the products have read the last ones, X when y has
+            if (c >= 2 && (!wait2(B_D, c - 2) || (OUT && !wait2(B_G, c - 2)))) break;
+            if (lane == 0) {
+                bar_expect(full, (OUT ? 2 : 1) * L::kOp);
+#pragma unroll
+                for (int i = 0; i < N / 64; i++) tma_load(st + L::kB + i * 16384, &mb, g * N + i * 64, t, full);
+                if (OUT)
+#pragma unroll
+                    for (int i = 0; i < N / 64; i++) tma_load(st + L::kC + i * 16384, &mc, g * N + i * 64, t, full);
             }
-            fence_async();
+            half = 1;
+            if (c >= 2 && !wait2(B_E, c - 2)) break;
+            if (lane == 0) {
+                bar_expect(full, L::kX);
+                tma_load(st + L::kXs, &mx, h * p.dv + c0, t, full);
+                // the chunk that has no stage yet: from DRAM to L2 (C and B come for the
+                // first of their heads only)
+                if (c + 2 < chunks) tma_prefetch(&mx, h * p.dv + c0, t + 2 * kChunk);
+            }
+            half = 0;
+            issued = c + 1;
         }
-        tc_before();
-        if (!__syncthreads_and(ok)) { ok = false; break; }
-        if (OUT && tid == 0) {
-            tc_after();
-            const uint32_t c = smem_at(sm + L::kC), b = smem_at(sm + L::kB), s = smem_at(sm + L::kS);
-#pragma unroll
-            for (int k = 0; k < N / 16; k++)
-                mma_ss(tm + kG, mat(c + k / 4 * 16384 + k % 4 * 32, 16), mat(b + k / 4 * 16384 + k % 4 * 32, 16),
-                       ins(128, false, false), k > 0);
-#pragma unroll
-            for (int k = 0; k < N / 16; k++)
-                mma_ss(tm + kYo, mat(c + k / 4 * 16384 + k % 4 * 32, 16), mat(s + k * 2048, 16384),
-                       ins(64, false, true), k > 0);
-            tc_commit(bars + 1);
+        // no copy may outlive the CTA, whatever became of its readers
+        ok = true;
+        if (half && lane == 0) bar_arrive(bars + B_FULL + (issued & 1));     // without its X
+        issued += half;
+        for (int c = issued > 2 ? issued - 2 : 0; c < issued; c++) wait2(B_FULL, c);
+    } else if (warp >= 24) {
+        // ---------------------------------------------------- products
+        // descriptors of the first stage; what follows adds multiples of 16 bytes
+        const uint64_t bk = mat(smem_at(sm + L::kB), 16), ck = mat(smem_at(sm + L::kC), 16);
+        const uint64_t bn = mat(smem_at(sm + L::kB), 16384), xn = mat(smem_at(sm + L::kXs), 16384);
+        const uint64_t sn = mat(smem_at(sm + L::kS), 16384), wn = mat(smem_at(sm + L::kW0), 16384);
+        if (warp == 24) {
+            // what the states wait for: C S and the increment
+            for (int c = 0; c < chunks; c++) {
+                const uint64_t at = (uint64_t)((c & 1) * (L::kStage / 16));
+                const uint32_t yo = tm + kYo + (c & 1) * 64;
+                if (!wait2(B_FULL, c) || !wait(B_S, c)) break;   // S in shared memory, the increment read
+                tc_after();
+                if (OUT) {
+#pragma unroll 4
+                    for (int k = 0; k < N / 16; k++)
+                        mma_ss(yo, ck + at + k / 4 * 1024 + k % 4 * 2, sn + k * 128, ins(64, false, true), k > 0);
+                    tc_commit(bars + B_YO);
+                }
+                if (!wait2(B_W01, c)) break;
+                tc_after();
+#pragma unroll 4
+                for (int k = 0; k < 8; k++)
+                    mma_ss(tm + kD, bn + at + k * 128, wn + k * 128, ins(128, true, true), k > 0);
+                if (!wait(B_W2, c)) break;
+                tc_after();
+#pragma unroll 4
+                for (int k = 0; k < 8; k++)
+                    mma_ss(tm + kD, bn + at + k * 128, wn + 2 * (L::kX / 16) + k * 128, ins(64, true, true), 1);
+                tc_commit(bars + B_D + (c & 1));
+            }
+        } else if (OUT && chunks > 0) {
+            // M X of a chunk and G of the next: G first, which M waits for, where its
+            // operands are there
+            auto make_g = [&](int c) {
+                const uint64_t at = (uint64_t)((c & 1) * (L::kStage / 16));
+                if (!wait2(B_FULL, c)) return;
+                tc_after();
+#pragma unroll 4
+                for (int k = 0; k < N / 16; k++)
+                    mma_ss(tm + kG, ck + at + k / 4 * 1024 + k % 4 * 2, bk + at + k / 4 * 1024 + k % 4 * 2,
+                           ins(128, false, false), k > 0);
+                tc_commit(bars + B_G + (c & 1));
+            };
+            make_g(0);
+            for (int c = 0; c < chunks; c++) {
+                // M is there and G has been read; X's rows behind the last token are
+                // zero; the last y has been read
+                if (!wait(B_M, c)) break;
+                tc_after();
+                const bool next = c + 1 < chunks;
+                const bool early = next && __all_sync(~0u, bar_test(bars + B_FULL + (c + 1 & 1), (c + 1) >> 1 & 1));
+                if (early) make_g(c + 1);
+                if (!wait2(B_W01, c) || (c > 0 && !wait2(B_E, c - 1))) break;
+                tc_after();
+                const uint64_t at = (uint64_t)((c & 1) * (L::kStage / 16));
+#pragma unroll 4
+                for (int k = 0; k < 8; k++)
+                    mma_ts(tm + kY, tm + kM + k * 8, xn + at + k * 128, ins(64, false, true), k > 0);
+                tc_commit(bars + B_Y);
+                if (next && !early) make_g(c + 1);
+            }
         }
-        if (OUT) {
-            ok = bar_wait(bars + 1, par);
-            tc_after();
+        if (!ok) {
+            // products in flight end before tensor memory is given back
+            __syncwarp();
+            tc_commit(bars + B_DRAIN + (warp & 1));
+            (void)bar_wait(bars + B_DRAIN + (warp & 1), 0);
         }
-        // w X in three parts: row r, pieces half * 4 ..
-        {
-            const int r = tid & 127, blk = r / 32;
+    } else if (warp >= 16) {
+        // ---------------------------------------------------- W: half of row `r` of X
+        const int wt = tid - 16 * 32, r = wt & 127, half = wt >> 7;
+        constexpr int kPieces = 4;                               // 16-byte pieces of half a row
+        for (int c = 0; c < chunks; c++) {
+            const int64_t t0 = seg.from + (int64_t)c * kChunk;
+            const int valid = seg.to - t0 < kChunk ? (int)(seg.to - t0) : kChunk;
+            const Scalars& sc = scal[c % 3];
+            if (!wait3(B_SC, c) || !wait2(B_FULL, c)) break;
+            unsigned char* const st = sm + (c & 1) * L::kStage;
+            if (valid < kChunk) {
+                // rows of other sequences or of nothing: zero, whatever they hold
+                for (int i = wt; i < (kChunk - valid) * (N / 8 + 8); i += 256) {
+                    const int q = valid + i / (N / 8 + 8), e = i % (N / 8 + 8);
+                    unsigned char* at = e < N / 8 ? st + L::kB + e / 8 * 16384 + q * 128 + e % 8 * 16
+                                                  : st + L::kXs + q * 128 + (e - N / 8) * 16;
+                    *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+                }
+                // the last chunk: the one phase of this barrier
+                fence_async();
+                warp_arrive(bars + B_WSYNC, lane);
+                if (!wait(B_WSYNC, 0)) break;
+            }
             float w = sc.behind[r];
 #pragma unroll
             for (int u = 1; u < 4; u++)
-                if (u > blk) w *= sc.block[u];
-            float probe = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                const int at = swz(r, half * 4 + c);
-                const uint4 v = *reinterpret_cast<const uint4*>(sm + L::kXs + at);
+                if (u > r / 32) w *= sc.block[u];
+            // part k of the piece `v` (each remainder is exact), and a probe that is NaN
+            // where x is not a finite number
+            f2 probe = 0;
+            auto split = [&](const uint4& v, uint4 (&o)[3]) {
                 const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[3][4];
+                uint32_t q[3][4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const float xa = bf_lo(in[i]), xb = bf_hi(in[i]);
-                    probe = fmaf(xa, 0.0f, probe);
-                    probe = fmaf(xb, 0.0f, probe);
-                    float pa = w * xa, pb = w * xb;
-                    o[0][i] = pack_bf(pa, pb);
-                    pa -= bf_lo(o[0][i]);
-                    pb -= bf_hi(o[0][i]);
-                    o[1][i] = pack_bf(pa, pb);
-                    pa -= bf_lo(o[1][i]);
-                    pb -= bf_hi(o[1][i]);
-                    o[2][i] = pack_bf(pa, pb);
+                    const f2 xv = bf_pair(in[i]);
+                    probe = fma2(xv, 0ull, probe);
+                    f2 t = mul2(xv, pair(w, w));
+                    q[0][i] = pack_bf(t);
+                    t = fma2(bf_pair(q[0][i]), pair(-1.0f, -1.0f), t);
+                    q[1][i] = pack_bf(t);
+                    q[2][i] = pack_bf(fma2(bf_pair(q[1][i]), pair(-1.0f, -1.0f), t));
                 }
-                *reinterpret_cast<uint4*>(sm + L::kW0 + at) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-                *reinterpret_cast<uint4*>(sm + L::kW1 + at) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-                *reinterpret_cast<uint4*>(sm + L::kW2 + at) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+#pragma unroll
+                for (int k = 0; k < 3; k++) o[k] = make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
+            };
+            if (c >= 1 && !wait2(B_D, c - 1)) break;              // the last parts have been multiplied
+            uint4 lo[kPieces];
+#pragma unroll
+            for (int e = 0; e < kPieces; e++) {
+                const int at = swz(r, half * 4 + e);
+                uint4 o[3];
+                split(*reinterpret_cast<const uint4*>(st + L::kXs + at), o);
+                *reinterpret_cast<uint4*>(sm + L::kW0 + at) = o[0];
+                *reinterpret_cast<uint4*>(sm + L::kW1 + at) = o[1];
+                lo[e] = o[2];
             }
-            if (OUT && probe != probe) {
+            const float2 pr = unpair(probe);
+            if (OUT && pr.x + pr.y != 0.0f) {
                 // a non-finite x must not reach earlier rows through M's zeros: it
                 // leaves X, and its column becomes NaN from its row on
-                for (int c = 0; c < 4; c++)
+                for (int e = 0; e < kPieces; e++)
                     for (int i = 0; i < 8; i++) {
-                        uint16_t* e = reinterpret_cast<uint16_t*>(sm + L::kXs + swz(r, half * 4 + c)) + i;
-                        if ((*e & 0x7f80) == 0x7f80) {
-                            *e = 0;
-                            atomicMin(bad + half * 32 + c * 8 + i, r);
+                        uint16_t* at = reinterpret_cast<uint16_t*>(st + L::kXs + swz(r, half * 4 + e)) + i;
+                        if ((*at & 0x7f80) == 0x7f80) {
+                            *at = 0;
+                            atomicMin(bad + (c & 1) * 64 + (half * 4 + e) * 8 + i, r);
                         }
                     }
             }
+            fence_async();
+            warp_arrive(bars + B_W01 + (c & 1), lane);
+            // the third part's place is S's until S has been multiplied
+            if (OUT && !wait(B_YO, c)) break;
+#pragma unroll
+            for (int e = 0; e < kPieces; e++) *reinterpret_cast<uint4*>(sm + L::kW2 + swz(r, half * 4 + e)) = lo[e];
+            fence_async();
+            warp_arrive(bars + B_W2, lane);
         }
-        if (OUT) {
-            // M, two 32 x 32 blocks a warp: row `row`, columns b * 32 ..
+    } else if (warp >= 8) {
+        // ---------------------------------------------------- M: row `row`
+        // (warps 8 to 11: the blocks left of its own; 12 to 15: its own, and the decays)
+        const int row = quad * 32 + lane;
+        const bool own = warp >= 12;
+        const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
+        auto fetch = [&](int c) {
+            const int64_t t = seg.from + (int64_t)c * kChunk + row;
+            // as it lies in memory: a conversion here would wait for the load
+            if (t >= seg.to) return 0u;
+            const int64_t i = t * p.dts + h;
+            return p.dt_bf16 ? (uint32_t)__ldg(static_cast<const uint16_t*>(p.dt) + i) : __ldg(static_cast<const uint32_t*>(p.dt) + i);
+        };
+        uint32_t raw_dt = fetch(0);
+        auto decays = [&](int c) {
+            Scalars& sc = scal[c % 3];
+            const bool in = seg.from + (int64_t)c * kChunk + row < seg.to;
+            const float raw = __uint_as_float(p.dt_bf16 ? raw_dt << 16 : raw_dt);
+            const float dt = in ? time_step(raw, bias, p.softplus) : 0.0f, a = in ? expf(dt * A) : 1.0f;
+            float up = a, down = a;
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int b = e * 2 + half;
-                uint32_t m[16];
-                if (b > quad) {
+            for (int d = 1; d < 32; d <<= 1) {
+                const float u = __shfl_up_sync(~0u, up, d), v = __shfl_down_sync(~0u, down, d);
+                if (lane >= d) up *= u;
+                if (lane + d < 32) down *= v;
+            }
+            float behind = __shfl_down_sync(~0u, down, 1);
+            if (lane == 31) behind = 1.0f;
+            sc.a[row] = a;
+            sc.dt[row] = dt;
+            sc.upto[row] = up;
+            sc.behind[row] = behind * dt;
+            if (lane == 31) sc.block[quad] = up;
+            warp_arrive(bars + B_SC + c % 3, lane);
+            raw_dt = fetch(c + 1);
+        };
+        for (int c = 0; c < 2 && c < chunks && own; c++) decays(c);
+        // M of a chunk, then the decays two chunks ahead (three places: no one reads
+        // this one any more)
+        for (int c = 0; c < chunks; c++) {
+            if constexpr (OUT) {
+                const Scalars& sc = scal[c % 3];
+                if (!wait3(B_SC, c) || !wait2(B_G, c) || (c > 0 && !wait(B_Y, c - 1))) break;
+                tc_after();
+#pragma unroll 1
+                for (int b = 0; b < quad && !own; b++) {
+                    float f = sc.upto[row];
+#pragma unroll 1
+                    for (int u = b + 1; u < quad; u++) f *= sc.block[u];
+                    float v[2][16];
+                    tm_load16(tq + kG + b * 32, tq + kG + b * 32 + 16, v[0], v[1]);
+                    const float4* behind = reinterpret_cast<const float4*>(sc.behind + b * 32);
 #pragma unroll
-                    for (int i = 0; i < 16; i++) m[i] = 0;
-                } else {
-                    float v[32];
-                    tm_load32(tq + kG + b * 32, v);
-                    if (b == quad) {
-                        float f = 1.0f;                   // P(row, j) for j = 31 .. 0
+                    for (int e = 0; e < 2; e++) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int j = 31; j >= 0; j--) {
-                            const float fd = f * sc.dt[b * 32 + j];
-                            v[j] = j <= lane ? v[j] * fd : 0.0f;
-                            f = j <= lane ? f * sc.a[b * 32 + j] : f;
+                        for (int j = 0; j < 4; j++) {
+                            const float4 q = behind[e * 4 + j];
+                            o[2 * j] = pack_bf(mul2(pair(v[e][4 * j], v[e][4 * j + 1]), mul2(pair(f, f), pair(q.x, q.y))));
+                            o[2 * j + 1] = pack_bf(mul2(pair(v[e][4 * j + 2], v[e][4 * j + 3]), mul2(pair(f, f), pair(q.z, q.w))));
                         }
-                    } else {
-                        float f = sc.upto[row];
-#pragma unroll
-                        for (int u = 1; u < 3; u++)
-                            if (u > b && u < quad) f *= sc.block[u];
-#pragma unroll
-                        for (int j = 0; j < 32; j++) v[j] *= f * sc.behind[b * 32 + j];
+                        tm_store8(tq + kM + b * 16 + e * 8, o);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) m[i] = pack_bf(v[2 * i], v[2 * i + 1]);
                 }
-                tm_store16(tq + kM + b * 16, m);
+                if (own) {
+                    // its own block, from the right: P(row, j) for j = 31 .. 0
+                    float v[2][16], e = 1.0f;
+                    tm_load16(tq + kG + quad * 32, tq + kG + quad * 32 + 16, v[0], v[1]);
+#pragma unroll
+                    for (int b = 1; b >= 0; b--) {
+                        const float4* dts = reinterpret_cast<const float4*>(sc.dt + quad * 32 + b * 16);
+                        const float4* as = reinterpret_cast<const float4*>(sc.a + quad * 32 + b * 16);
+                        uint32_t o[8];
+#pragma unroll
+                        for (int j = 3; j >= 0; j--) {
+                            const float4 t4 = dts[j], a4 = as[j];
+                            const float t[4] = {t4.x, t4.y, t4.z, t4.w}, a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+                            for (int i = 3; i >= 0; i--) {
+                                const bool in = b * 16 + 4 * j + i <= lane;
+                                float& u = v[b][4 * j + i];
+                                u = in ? u * (e * t[i]) : 0.0f;
+                                e = in ? e * a[i] : e;
+                            }
+                            o[2 * j] = pack_bf(v[b][4 * j], v[b][4 * j + 1]);
+                            o[2 * j + 1] = pack_bf(v[b][4 * j + 2], v[b][4 * j + 3]);
+                        }
+                        tm_store8(tq + kM + quad * 16 + b * 8, o);
+                    }
+                    {
+                        const uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+                        for (int b = 2 * quad + 2; b < 8; b++) tm_store8(tq + kM + b * 8, o);
+                    }
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_before();
+                warp_arrive(bars + B_M, lane);
             }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            if (own && c + 2 < chunks) {
+                if (c >= 1 && !wait2(B_E, c - 1)) break;
+                decays(c + 2);
+            }
         }
-        fence_async();
-        tc_before();
-        if (!__syncthreads_and(ok)) { ok = false; break; }
-        if (tid == 0) {
-            tc_after();
-            const uint32_t b = smem_at(sm + L::kB), x = smem_at(sm + L::kXs);
-            const uint32_t w[3] = {smem_at(sm + L::kW0), smem_at(sm + L::kW1), smem_at(sm + L::kW2)};
-            if (OUT)
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    mma_ts(tm + kY, tm + kM + k * 8, mat(x + k * 2048, 16384), ins(64, false, true), k > 0);
-#pragma unroll
-            for (int i = 2; i >= 0; i--)
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    mma_ss(tm + kD, mat(b + k * 2048, 16384), mat(w[i] + k * 2048, 16384), ins(64, true, true),
-                           i < 2 || k > 0);
-            tc_commit(bars + 2);
-        }
-        // while the products run: the next chunk's decays, and x for D x
-        const bool more = t0 + kChunk < seg.to;
-        if (more) scalars(t0 + kChunk, scal[par ^ 1]);
-        if (t0 + 2 * kChunk < seg.to) fetch_dt(t0 + 2 * kChunk);
-        uint4 xr[4];
-        if (OUT)
-#pragma unroll
-            for (int c = 0; c < 4; c++) xr[c] = *reinterpret_cast<const uint4*>(sm + L::kXs + swz(row, half * 4 + c));
-        __syncthreads();                       // X has been read
-        ok = bar_wait(bars + 2, par);
-        tc_after();
-        if (ok && more && tid == 0) load(t0 + kChunk);
+    } else {
+        // ---------------------------------------------------- E: half of row `row` of S and of y
+        const int row = quad * 32 + lane, half = warp >> 2;
+        const bool holds = row < N;
+        const float D = OUT && p.D ? p.D[h] : 0.0f;
+        const int64_t tile = (int64_t)N * p.dv, mine = (int64_t)row * p.dv + c0 + half * 32;
+        f2 S[16];
         {
-            float v[32];
-            tm_load32(tq + kD + half * 32, v);
+            const float* from = nullptr;
+            if (OUT && p.cut) from = p.seg_state + ((int64_t)blockIdx.x * p.heads + h) * tile + mine;
+            else if (OUT && p.initial) from = p.state + ((int64_t)seg.sequence * p.heads + h) * tile + mine;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                float4 v = make_float4(0, 0, 0, 0);
+                if (from && holds) v = *reinterpret_cast<const float4*>(from + 2 * i);
+                S[i] = pair(v.x, v.y);
+                S[i + 1] = pair(v.z, v.w);
+            }
+        }
+        auto put_state = [&] {
+            if (OUT && holds)
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    *reinterpret_cast<uint4*>(sm + L::kS + swz(row, half * 4 + c)) =
+                        make_uint4(pack_bf(S[c * 4]), pack_bf(S[c * 4 + 1]), pack_bf(S[c * 4 + 2]), pack_bf(S[c * 4 + 3]));
+            fence_async();
+            tc_before();
+            warp_arrive(bars + B_S, lane);
+        };
+        put_state();
+        float total = 1.0f;
+        int c = 0;
+        for (; c < chunks; c++) {
+            const Scalars& sc = scal[c % 3];
+            if (!wait3(B_SC, c) || !wait2(B_D, c)) break;
+            tc_after();
             const float dec = sc.block[0] * sc.block[1] * (sc.block[2] * sc.block[3]);
             if (!OUT) total *= dec;
 #pragma unroll
-            for (int i = 0; i < 32; i++) S[i] = fmaf(S[i], dec, v[i]);
-            if (more) put_state();
-        }
-        if (OUT) {
-            float v[32], o[32];
-            tm_load32(tq + kY + half * 32, v);
-            tm_load32(tq + kYo + half * 32, o);
+            for (int e = 0; e < 2; e++) {
+                float v[16], o[16];
+                tm_load16(tq + kD + half * 32 + e * 16, tq + kD + 64 + half * 32 + e * 16, v, o);
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    S[e * 8 + i] = fma2(S[e * 8 + i], pair(dec, dec),
+                                        add2(pair(v[2 * i], v[2 * i + 1]), pair(o[2 * i], o[2 * i + 1])));
+            }
+            put_state();
+            if (!OUT) {
+                warp_arrive(bars + B_E + (c & 1), lane);
+                continue;
+            }
             float f = sc.upto[row];
 #pragma unroll
             for (int u = 0; u < 3; u++)
                 if (u < quad) f *= sc.block[u];
+            if (!wait(B_Y, c)) break;
+            tc_after();
+            const unsigned char* const xs = sm + (c & 1) * L::kStage + L::kXs;
+            const int64_t t = seg.from + (int64_t)c * kChunk + row;
+            bf16* const y = static_cast<bf16*>(p.y) + t * p.ys + (int64_t)h * p.dv + c0 + half * 32;
+            const bool wide = (reinterpret_cast<uintptr_t>(y) & 31) == 0;
 #pragma unroll
-            for (int i = 0; i < 32; i++) v[i] = fmaf(f, o[i], v[i]);
+            for (int e = 0; e < 2; e++) {
+                uint32_t out[8];
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                const uint32_t in[4] = {xr[c].x, xr[c].y, xr[c].z, xr[c].w};
+                for (int q = 0; q < 2; q++) {
+                    float v[8], o[8];
+                    const uint32_t col = half * 32 + e * 16 + q * 8;
+                    tm_load8(tq + kYo + (c & 1) * 64 + col, tq + kY + col, o, v);
+                    const uint4 x4 = *reinterpret_cast<const uint4*>(xs + swz(row, half * 4 + e * 2 + q));
+                    const uint32_t in[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    v[c * 8 + 2 * i] = fmaf(D, bf_lo(in[i]), v[c * 8 + 2 * i]);
-                    v[c * 8 + 2 * i + 1] = fmaf(D, bf_hi(in[i]), v[c * 8 + 2 * i + 1]);
+                    for (int i = 0; i < 4; i++) {
+                        const f2 u = fma2(pair(f, f), pair(o[2 * i], o[2 * i + 1]), pair(v[2 * i], v[2 * i + 1]));
+                        out[q * 4 + i] = pack_bf(fma2(pair(D, D), bf_pair(in[i]), u));
+                    }
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i++)
-                if (row >= bad[half * 32 + i]) v[i] = __uint_as_float(0x7fc00000u);
-            if (row < valid) {
-                bf16* const y = static_cast<bf16*>(p.y) + (t0 + row) * p.ys + (int64_t)h * p.dv + c0 + half * 32;
-                if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
-#pragma unroll
-                    for (int c = 0; c < 4; c++)
-                        *reinterpret_cast<uint4*>(y + c * 8) =
-                            make_uint4(pack_bf(v[c * 8], v[c * 8 + 1]), pack_bf(v[c * 8 + 2], v[c * 8 + 3]),
-                                       pack_bf(v[c * 8 + 4], v[c * 8 + 5]), pack_bf(v[c * 8 + 6], v[c * 8 + 7]));
+                if (t >= seg.to) continue;
+                if (wide) {
+                    store32(y + e * 16, out);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i++) y[i] = __float2bfloat16_rn(v[i]);
+                    for (int i = 0; i < 8; i++) {
+                        reinterpret_cast<uint16_t*>(y)[e * 16 + 2 * i] = (uint16_t)out[i];
+                        reinterpret_cast<uint16_t*>(y)[e * 16 + 2 * i + 1] = (uint16_t)(out[i] >> 16);
+                    }
                 }
             }
+            // columns with a non-finite x, from its row on (128: none)
+            const int b0 = bad[(c & 1) * 64 + half * 32 + lane];
+            uint32_t nans = 0;                                   // of this row
+            if (__any_sync(~0u, b0 < kChunk)) {
+#pragma unroll 1
+                for (int j = 0; j < 32; j++) nans |= (uint32_t)(row >= __shfl_sync(~0u, b0, j)) << j;
+            }
+            tc_before();
+            warp_arrive(bars + B_E + (c & 1), lane);             // stage, decays, C S and M X have been read
+            if (t < seg.to) {
+#pragma unroll 1
+                for (; nans; nans &= nans - 1) reinterpret_cast<uint16_t*>(y)[__ffs((int)nans) - 1] = 0x7fc0;
+            }
         }
+        if (!ok) {
+            // a wait ran out (a GPU preempted for seconds): what is left is NaN
+            total = __uint_as_float(0x7fc00000u);
+#pragma unroll
+            for (int i = 0; i < 16; i++) S[i] = pair(total, total);
+            if (OUT)
+                for (int64_t t = seg.from + (int64_t)c * kChunk + row; t < seg.to; t += kChunk)
+                    for (int i = 0; i < 32; i++)
+                        static_cast<bf16*>(p.y)[t * p.ys + (int64_t)h * p.dv + c0 + half * 32 + i] = __float2bfloat16_rn(total);
+        }
+        float* to = nullptr;
+        if (!OUT) to = p.seg_state + ((int64_t)blockIdx.x * p.heads + h) * tile + mine;
+        else if (seg.last && p.state) to = p.state + ((int64_t)seg.sequence * p.heads + h) * tile + mine;
+        if (to && holds) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float2 u = unpair(S[i]), v = unpair(S[i + 1]);
+                *reinterpret_cast<float4*>(to + 2 * i) = make_float4(u.x, u.y, v.x, v.y);
+            }
+        }
+        if (!OUT && tid == 0 && c0 == 0) p.seg_decay[(int64_t)blockIdx.x * p.heads + h] = total;
+        tc_before();
     }
-    const bool all = __syncthreads_and(ok);
-    if (!all) {
-        // a wait ran out (a GPU preempted for seconds): what is left is NaN
-        for (int i = 0; i < 32; i++) S[i] = total = __uint_as_float(0x7fc00000u);
-        if (OUT)
-            for (int64_t t = t0 + (tid & 127); t < seg.to; t += kChunk)
-                for (int i = 0; i < 32; i++)
-                    static_cast<bf16*>(p.y)[t * p.ys + (int64_t)h * p.dv + c0 + half * 32 + i] = __float2bfloat16_rn(S[0]);
-    }
-    tc_before();
     __syncthreads();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmem) : "memory");
-    float* to = nullptr;
-    if (!OUT) to = p.seg_state + ((int64_t)blockIdx.x * p.heads + h) * N * p.dv;
-    else if (seg.last && p.state) to = p.state + ((int64_t)seg.sequence * p.heads + h) * N * p.dv;
-    if (to && holds) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(to + (int64_t)row * p.dv + c0 + half * 32 + i) =
-                make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-    }
-    if (!OUT && tid == 0 && c0 == 0) p.seg_decay[(int64_t)blockIdx.x * p.heads + h] = total;
 }
 
 // ------------------------------------------------------------ host
@@ -502,7 +731,7 @@ bool launch_chunk(const ScanParams& p, const CUtensorMap (&m)[3], int64_t segmen
     constexpr int bytes = ChunkSmem<N, OUT>::kBytes;
     if (!allow_smem(reinterpret_cast<const void*>(chunk_kernel<N, OUT>), bytes, done)) return false;
     const dim3 grid((unsigned)segments, (unsigned)(p.heads * (p.dv / 64)));
-    chunk_kernel<N, OUT><<<grid, 256, bytes, st>>>(p, m[0], m[1], m[2]);
+    chunk_kernel<N, OUT><<<grid, kThreads, bytes, st>>>(p, m[0], m[1], m[2]);
     return true;
 }
 
