@@ -4,9 +4,9 @@
 // The arithmetic is the dynamic rule of qstate.h on a fresh state (scale =
 // cvt(max / Qmax), code = clamp(round_half_even(S * inv)), the product exact),
 // bit for bit.  Bound: memory (four bytes read, bits / 8 written an element).  A
-// CTA takes one tile and holds it in registers: a thread eight consecutive
-// columns at a time, so that one scale of a whole tile (group 0) costs no second
-// read.  A group's lanes are joined by shuffles.
+// CTA takes a tile, or a part of one where groups lie inside a row, and holds it in
+// registers: a thread eight consecutive columns at a time, so that one scale of a
+// whole tile (group 0) costs no second read.  A group's lanes are joined by shuffles.
 #include "qmixer_common.cuh"
 
 namespace qm {
@@ -25,27 +25,20 @@ struct QuantParams {
     uint32_t head_off[kMaxMixedHeads];
 };
 
-// x * inv rounded half to even from the exact product: the error of the rounded
-// product decides where it lies on a tie.
-__device__ __forceinline__ int code_of(float x, float inv, float qmax) {
-    const float w = __fmul_rn(x, inv);
-    if (!(fabsf(w) < qmax + 1.0f)) return (int)copysignf(qmax, w);
-    const float e = fmaf(x, inv, -w);               // exact
-    float r = rintf(w);
-    const float d = w - r;                          // exact, |d| <= 1/2
-    if (fabsf(d) == 0.5f && e != 0.0f) {
-        // w lies on a tie and the product beside it
-        const float up = r + (d > 0.0f ? 1.0f : 0.0f), down = up - 1.0f;
-        r = e > 0.0f ? up : down;
-    }
-    return (int)fminf(fmaxf(r, -qmax), qmax);
+// x * inv rounded half to even from the exact product, as the low bits of the
+// result: one fused multiply-add to 1.5 * 2^23 rounds it once.
+__device__ __forceinline__ uint32_t code_of(float x, float inv, float qmax) {
+    constexpr float kMagic = 12582912.0f;
+    return __float_as_uint(fminf(fmaxf(fmaf(x, inv, kMagic), kMagic - qmax), kMagic + qmax));
 }
 
-template <int DK, int DV>
+// PARTS: CTAs that share a tile (one where a scale is of the whole tile).
+template <int DK, int DV, int PARTS>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantParams p) {
-    constexpr int kVecs = DK * DV / 8, kEach = kVecs / 256, kRow = DV / 8;
+    constexpr int kEach = DK * DV / 8 / 256 / PARTS, kRow = DV / 8;
     __shared__ uint32_t tops[8];                    // the warps' maxima
-    const int64_t tile = blockIdx.x;
+    const int64_t tile = blockIdx.x / PARTS;
+    const int u0 = (int)(blockIdx.x % PARTS) * (kEach * 256) + threadIdx.x;     // its first eight columns
     const int h = int(tile % p.heads);
     const int64_t row = tile / p.heads;
     const int bits = p.mixed ? p.head_bits[h] : p.bits;
@@ -53,7 +46,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     const float* const S = p.S + tile * (DK * DV);
     float v[kEach][8];
 #pragma unroll
-    for (int i = 0; i < kEach; i++) load8(S + (i * 256 + threadIdx.x) * 8, v[i]);
+    for (int i = 0; i < kEach; i++) load8(S + (i * 256 + u0) * 8, v[i]);
     if (p.rotate) {
         // the butterfly of qstate.h along d_v, one rounding per sum; a row is
         // kRow neighbouring lanes of eight columns
@@ -80,12 +73,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     }
     if (p.ref) {
 #pragma unroll
-        for (int i = 0; i < kEach; i++) store8(p.ref + tile * (DK * DV) + (i * 256 + threadIdx.x) * 8, v[i]);
+        for (int i = 0; i < kEach; i++) store8(p.ref + tile * (DK * DV) + (i * 256 + u0) * 8, v[i]);
     }
     if (bits == 32) {
 #pragma unroll
         for (int i = 0; i < kEach; i++)
-            store8(reinterpret_cast<float*>(codes) + (i * 256 + threadIdx.x) * 8, v[i]);
+            store8(reinterpret_cast<float*>(codes) + (i * 256 + u0) * 8, v[i]);
         return;
     }
     uint32_t m[kEach];
@@ -117,7 +110,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     const int per_row = p.group ? DV / p.group : 1;
 #pragma unroll
     for (int i = 0; i < kEach; i++) {
-        const int u = i * 256 + threadIdx.x, r = u / kRow, c8 = u % kRow;
+        const int u = i * 256 + u0, r = u / kRow, c8 = u % kRow;
         float scale = __fdiv_rn(__uint_as_float(m[i]), qmax);
         if (!p.scale_f32) scale = fminf(__half2float(__float2half_rn(scale)), 65504.0f);
         const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale);
@@ -127,31 +120,39 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
             if (p.scale_f32) static_cast<float*>(p.scales)[at] = scale;
             else static_cast<__half*>(p.scales)[at] = __float2half_rn(scale);
         }
-        int c[8];
+        uint32_t c[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) c[j] = code_of(v[i][j], inv, qmax);
         uint32_t lo = 0, hi = 0;
         if (bits == 8) {
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                lo |= (uint32_t)(c[j] & 255) << (8 * j);
-                hi |= (uint32_t)(c[j + 4] & 255) << (8 * j);
+                lo |= (c[j] & 255) << (8 * j);
+                hi |= (c[j + 4] & 255) << (8 * j);
             }
             *reinterpret_cast<uint2*>(codes + u * 8) = make_uint2(lo, hi);
         } else if (bits == 2) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) lo |= (uint32_t)(c[j] & 3) << (2 * j);
+            for (int j = 0; j < 8; j++) lo |= (c[j] & 3) << (2 * j);
             *reinterpret_cast<uint16_t*>(codes + u * 2) = (uint16_t)lo;
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                lo |= (uint32_t)(c[j] & 15) << (4 * j);
-                hi |= (uint32_t)((c[j] >> 4) & 3) << (2 * j);
+                lo |= (c[j] & 15) << (4 * j);
+                hi |= ((c[j] >> 4) & 3) << (2 * j);
             }
             *reinterpret_cast<uint32_t*>(codes + u * 4) = lo;
             if (bits == 6) *reinterpret_cast<uint16_t*>(codes + DK * DV / 2 + u * 2) = (uint16_t)hi;
         }
     }
+}
+
+// Groups are of a row: a tile then falls into pieces of 256 threads, for as many
+// loads in flight as may be (and one small tile over several SMs).
+template <int DK, int DV> void launch_quantize(const QuantParams& p, int64_t tiles, cudaStream_t st) {
+    constexpr int kParts = DK * DV / 8 / 256;
+    if (p.group) quantize_kernel<DK, DV, kParts><<<(unsigned)(tiles * kParts), 256, 0, st>>>(p);
+    else quantize_kernel<DK, DV, 1><<<(unsigned)tiles, 256, 0, st>>>(p);
 }
 
 bool width_ok(int b) { return b == 2 || b == 4 || b == 6 || b == 8; }
@@ -201,11 +202,12 @@ extern "C" int qmixer_quantize(const qmixer_quantize_args* args, qstate_stream s
         p.row_bytes = off;
         p.tile_bytes = 0;
     }
-    const unsigned tiles = (unsigned)(a.rows * a.heads);
+    const int64_t tiles = a.rows * a.heads;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (a.d_k == 64 && a.d_v == 64) qm::quantize_kernel<64, 64><<<tiles, 256, 0, st>>>(p);
-    else if (a.d_k == 64) qm::quantize_kernel<64, 128><<<tiles, 256, 0, st>>>(p);
-    else if (a.d_v == 64) qm::quantize_kernel<128, 64><<<tiles, 256, 0, st>>>(p);
-    else qm::quantize_kernel<128, 128><<<tiles, 256, 0, st>>>(p);
+    if (tiles * (a.d_k * a.d_v / 2048) > INT32_MAX) return QSTATE_EUNSUPPORTED;
+    if (a.d_k == 64 && a.d_v == 64) qm::launch_quantize<64, 64>(p, tiles, st);
+    else if (a.d_k == 64) qm::launch_quantize<64, 128>(p, tiles, st);
+    else if (a.d_v == 64) qm::launch_quantize<128, 64>(p, tiles, st);
+    else qm::launch_quantize<128, 128>(p, tiles, st);
     return qm::launched();
 }

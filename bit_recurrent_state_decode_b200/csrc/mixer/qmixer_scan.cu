@@ -63,23 +63,37 @@ int sm_count() {
     return n;
 }
 
-// Cut or not, by an estimate in tokens of one CTA's chain.  Uncut: the longest
-// chain, taken as up to four times the mean where the lengths are not known
-// here, or the whole work over the resident CTAs.  Cut: the work with launch 1
-// on top.
+// Where to cut, by an estimate of the time in tokens of one CTA's chain.
+// `resident` chains run at once; launch 1 takes kStates of launch 3 (measured 0.41
+// for the chunked form, 0.6 for the recurrent one), the launches kLaunch tokens.
+//   equal sequences: whole rounds of resident CTAs, each as long as a segment
+//   unequal ones:    the work spread evenly, and the last segment behind it; the
+//                    longest uncut sequence is taken as four times the mean (the
+//                    lengths lie on the device)
 ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, int dtype, bool ragged, int sms) {
-    const int64_t unit = dtype == QSTATE_BF16 ? kChunk : kBatchTokens;
-    // CTAs that an SM holds: two of the recurrent form, one of the chunked
-    const int64_t chains = (int64_t)heads * (dv / 64), resident = (dtype == QSTATE_BF16 ? 1 : 2) * sms;
+    const bool chunked = dtype == QSTATE_BF16;
+    const int64_t unit = chunked ? kChunk : kBatchTokens;
+    const int64_t chains = (int64_t)heads * (dv / 64), resident = (chunked ? 1 : dk == 64 ? 4 : 2) * (int64_t)sms;
+    const double states = chunked ? 0.41 : 0.6, launches = chunked ? 4 * kChunk : 2 * kBatchTokens;
     const int64_t mean = tokens / sequences, longest = ragged ? (4 * mean < tokens ? 4 * mean : tokens) : mean;
-    const int64_t even = tokens * chains / resident;
     ScanPlan o{};
     o.seg_len = tokens > 0 ? tokens : 1;
-    int64_t len = (even + unit - 1) / unit * unit;
-    if (len < 2 * unit) len = 2 * unit;
-    if (16 * len + 8 * unit < 10 * longest) {        // 1.6 times the work, two launches
-        o.cut = true;
-        o.seg_len = len;
+    double best = 0.0;
+    for (int k = 1; k <= 64; k++) {
+        // k segments of the longest sequence
+        const int64_t len = ((longest + k - 1) / k + unit - 1) / unit * unit;
+        if (k > 1 && len < 2 * unit) break;
+        const int64_t each = len > 0 ? (mean + len - 1) / len : 1;
+        double time;
+        if (ragged) time = (double)tokens * chains / resident + 0.5 * len;
+        else time = (double)((sequences * chains * each + resident - 1) / resident) * len;
+        if (ragged && time < len) time = (double)len;
+        if (k > 1) time = time * (1.0 + states) + launches;
+        if (k == 1 || time < best) {
+            best = time;
+            o.cut = k > 1;
+            if (k > 1) o.seg_len = len;
+        }
     }
     o.segments = o.cut ? tokens / o.seg_len + sequences : sequences;
     if (o.cut) {
@@ -141,10 +155,11 @@ int qmixer_scan(const qmixer_scan_args* args, qstate_stream stream) {
                      plan.seg_len, plan.segments, plan.cut, static_cast<float*>(a.workspace),
                      plan.cut ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.state_bytes) : nullptr};
     const cudaStream_t st = (cudaStream_t)stream;
+    // (without tokens only states are set: any form does)
     const bool chunked = a.dtype == QSTATE_BF16 && a.tokens > 0;
     auto launch = [&](bool states_only) {
         if (chunked) return qm::launch_scan_chunk(p, a.d_k, plan.segments, states_only, st);
-        qm::launch_scan_rec(p, a.dtype, a.d_k, plan.segments, states_only, st);
+        qm::launch_scan_rec(p, a.d_k, plan.segments, states_only, st);
         return true;
     };
     if (plan.cut) {

@@ -99,9 +99,9 @@ __device__ __forceinline__ bool find_segment(const ScanParams& p, int64_t g, Seg
     return true;
 }
 
-// The kernels of the recurrent form (any type) and of the chunked form
-// (bfloat16, tensor cores): states only (launch 1) or the whole scan.
-void launch_scan_rec(const ScanParams& p, int dtype, int dk, int64_t segments, bool states_only, cudaStream_t st);
+// The kernels of the recurrent form (binary32) and of the chunked form (bfloat16,
+// tensor cores): states only (launch 1) or the whole scan.
+void launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
 bool launch_scan_chunk(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
 
 }  // namespace qm

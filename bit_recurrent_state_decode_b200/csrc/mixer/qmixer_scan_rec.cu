@@ -1,4 +1,5 @@
-// qmixer_scan_rec.cu -- the prompt scan token by token, in binary32 throughout:
+// qmixer_scan_rec.cu -- the prompt scan of binary32 inputs, token by token, in
+// binary32 throughout:
 // S <- a S + (dt x) B^T, y = S^T C + D x.
 //
 // A CTA takes 64 value columns of one head over one segment, with the state in
@@ -21,7 +22,7 @@ template <int N> struct RecSmem {
     float2 ad[2][kBatch];        // decay, time step
 };
 
-template <class T, int N, bool OUT>
+template <int N, bool OUT>
 __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
     constexpr int kThreads = N * 2, kL = N / 8;      // threads of one column group
     extern __shared__ __align__(16) unsigned char raw[];
@@ -63,11 +64,11 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
         na = 1.0f;
         nd = 0.0f;
         if (t0 + kr < seg.to) {
-            load8(static_cast<const T*>(p.B) + (t0 + kr) * p.Bs + (int64_t)g * N + kc, nk);
-            if (OUT) load8(static_cast<const T*>(p.C) + (t0 + kr) * p.Cs + (int64_t)g * N + kc, nq);
+            load8(static_cast<const float*>(p.B) + (t0 + kr) * p.Bs + (int64_t)g * N + kc, nk);
+            if (OUT) load8(static_cast<const float*>(p.C) + (t0 + kr) * p.Cs + (int64_t)g * N + kc, nq);
         }
         if (tid < 128 && t0 + xr < seg.to)
-            load8(static_cast<const T*>(p.x) + (t0 + xr) * p.xs + (int64_t)h * p.dv + c0 + xc, nx);
+            load8(static_cast<const float*>(p.x) + (t0 + xr) * p.xs + (int64_t)h * p.dv + c0 + xc, nx);
         if (tid < kBatch && t0 + tid < seg.to) {
             nd = time_step(load_dt(p.dt, (t0 + tid) * p.dts + h, p.dt_bf16), bias, p.softplus);
             na = expf(nd * A);
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
     for (int64_t t0 = seg.from; t0 < seg.to; t0 += kBatch, b ^= 1) {
         fetch(t0 + kBatch);
         const int n = seg.to - t0 < kBatch ? (int)(seg.to - t0) : kBatch;
-#pragma unroll 2
+#pragma unroll 4
         for (int t = 0; t < n; t++) {
             const float2 ad = sm.ad[b][t];
             const float4 xv = *reinterpret_cast<const float4*>(&sm.x[b][t][pg]);
@@ -136,12 +137,12 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
         if (OUT && tid < 128 && xr < n) {
             float o[8];
             load8(&sm.y[b][xr][xc], o);
-            T* const y = static_cast<T*>(p.y) + (t0 + xr) * p.ys + (int64_t)h * p.dv + c0 + xc;
+            float* const y = static_cast<float*>(p.y) + (t0 + xr) * p.ys + (int64_t)h * p.dv + c0 + xc;
             if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
                 store8(y, o);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; j++) y[j] = from_f32<T>(o[j]);
+                for (int j = 0; j < 8; j++) y[j] = o[j];
             }
         }
     }
@@ -160,28 +161,23 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
     if (!OUT && tid == 0 && c0 == 0) p.seg_decay[(int64_t)blockIdx.x * p.heads + h] = total;
 }
 
-template <class T, int N, bool OUT>
+template <int N, bool OUT>
 void launch_rec(const ScanParams& p, int64_t segments, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(reinterpret_cast<const void*>(rec_kernel<T, N, OUT>), sizeof(RecSmem<N>), done)) return;
+    if (!allow_smem(reinterpret_cast<const void*>(rec_kernel<N, OUT>), sizeof(RecSmem<N>), done)) return;
     const dim3 grid((unsigned)segments, (unsigned)(p.heads * (p.dv / 64)));
-    rec_kernel<T, N, OUT><<<grid, N * 2, sizeof(RecSmem<N>), st>>>(p);
+    rec_kernel<N, OUT><<<grid, N * 2, sizeof(RecSmem<N>), st>>>(p);
 }
 
-template <class T, int N>
+template <int N>
 void launch_rec(const ScanParams& p, int64_t segments, bool states_only, cudaStream_t st) {
-    if (states_only) launch_rec<T, N, false>(p, segments, st);
-    else launch_rec<T, N, true>(p, segments, st);
+    if (states_only) launch_rec<N, false>(p, segments, st);
+    else launch_rec<N, true>(p, segments, st);
 }
 
-void launch_scan_rec(const ScanParams& p, int dtype, int dk, int64_t segments, bool states_only, cudaStream_t st) {
-    if (dtype == QSTATE_BF16) {
-        if (dk == 64) launch_rec<bf16, 64>(p, segments, states_only, st);
-        else launch_rec<bf16, 128>(p, segments, states_only, st);
-    } else {
-        if (dk == 64) launch_rec<float, 64>(p, segments, states_only, st);
-        else launch_rec<float, 128>(p, segments, states_only, st);
-    }
+void launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st) {
+    if (dk == 64) launch_rec<64>(p, segments, states_only, st);
+    else launch_rec<128>(p, segments, states_only, st);
 }
 
 }  // namespace qm
