@@ -64,8 +64,10 @@ int sm_count() {
 }
 
 // Where to cut, by an estimate of the time in tokens of one CTA's chain.
-// `resident` chains run at once; launch 1 takes kStates of launch 3 (measured 0.41
-// for the chunked form, 0.6 for the recurrent one), the launches kLaunch tokens.
+// `resident` chains run at once; a CTA of the recurrent form takes a batch's time
+// before its first token (of 0 to 256 tokens tried for either form, this gave the
+// least over ragged and single prompts); launch 1 takes `states` of launch 3 (measured: 0.41 of the
+// chunked form, 0.6 of the recurrent one), and cutting two launches more.
 //   equal sequences: whole rounds of resident CTAs, each as long as a segment
 //   unequal ones:    the work spread evenly, and the last segment behind it; the
 //                    longest uncut sequence is taken as four times the mean (the
@@ -75,6 +77,7 @@ ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, int
     const int64_t unit = chunked ? kChunk : kBatchTokens;
     const int64_t chains = (int64_t)heads * (dv / 64), resident = (chunked ? 1 : dk == 64 ? 4 : 2) * (int64_t)sms;
     const double states = chunked ? 0.41 : 0.6, launches = chunked ? 4 * kChunk : 2 * kBatchTokens;
+    const int64_t start = chunked ? 0 : kBatchTokens;
     const int64_t mean = tokens / sequences, longest = ragged ? (4 * mean < tokens ? 4 * mean : tokens) : mean;
     ScanPlan o{};
     o.seg_len = tokens > 0 ? tokens : 1;
@@ -85,8 +88,8 @@ ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, int
         if (k > 1 && len < 2 * unit) break;
         const int64_t each = len > 0 ? (mean + len - 1) / len : 1;
         double time;
-        if (ragged) time = (double)tokens * chains / resident + 0.5 * len;
-        else time = (double)((sequences * chains * each + resident - 1) / resident) * len;
+        if (ragged) time = (double)tokens * chains / resident * (len + start) / (len > 0 ? len : 1) + 0.5 * len;
+        else time = (double)((sequences * chains * each + resident - 1) / resident) * (len + start);
         if (ragged && time < len) time = (double)len;
         if (k > 1) time = time * (1.0 + states) + launches;
         if (k == 1 || time < best) {

@@ -6,19 +6,20 @@
 // registers: a thread holds 8 rows x 4 columns as pairs of rows, so that B and C
 // come from shared memory as the pairs that the packed binary32 instructions take
 // (sm_100 issues two operations of a pair at once).  A token costs 48 packed
-// instructions, five 16-byte shared loads and the five shuffles that sum y over
-// the 8 or 16 threads of a column: about 75 instructions a thread, so
-// instruction issue is the bound, not memory.  kBatch tokens are staged at a
-// time while the next ones are on their way to registers.
+// instructions and five 16-byte shared loads a thread: instruction issue is the
+// bound, not memory.  kBatch tokens are staged at a time while the next ones are on
+// their way to registers.  The 8 or 16 threads of a column leave their parts of y in
+// shared memory, where they are added once per batch (shuffles within the token
+// took a fifth of the instructions and most of the waiting).
 #include "qmixer_scan.cuh"
 
 namespace qm {
 
-
 constexpr int kBatch = kBatchTokens;
 
 template <int N> struct RecSmem {
-    float k[2][kBatch][N], q[2][kBatch][N], x[2][kBatch][64], y[2][kBatch][64];
+    float k[2][kBatch][N], q[2][kBatch][N], x[2][kBatch][64];
+    float part[kBatch][N / 8][68];   // a row of 64 shifted by four banks against the next
     float2 ad[2][kBatch];        // decay, time step
 };
 
@@ -117,33 +118,38 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
                     const float2 u = unpair(s);
                     o[j] = u.x + u.y;
                 }
-                // sum over the column group's threads, scattering the four columns
-                const bool b0 = tid & 1, b1 = tid & 2;
-                float u0 = b0 ? o[2] : o[0], u1 = b0 ? o[3] : o[1];
-                u0 += __shfl_xor_sync(~0u, b0 ? o[0] : o[2], 1);
-                u1 += __shfl_xor_sync(~0u, b0 ? o[1] : o[3], 1);
-                float u = b1 ? u1 : u0;
-                u += __shfl_xor_sync(~0u, b1 ? u0 : u1, 2);
-#pragma unroll
-                for (int d = 4; d < kL; d <<= 1) u += __shfl_xor_sync(~0u, u, d);
-                if (tid % kL < 4) {
-                    const int c = pg + (b0 ? 2 : 0) + (b1 ? 1 : 0);
-                    sm.y[b][t][c] = fmaf(D, sm.x[b][t][c], u);
-                }
+                *reinterpret_cast<float4*>(&sm.part[t][tid % kL][pg]) = make_float4(o[0], o[1], o[2], o[3]);
             }
         }
         stage(b ^ 1);
         __syncthreads();
-        if (OUT && tid < 128 && xr < n) {
-            float o[8];
-            load8(&sm.y[b][xr][xc], o);
-            float* const y = static_cast<float*>(p.y) + (t0 + xr) * p.ys + (int64_t)h * p.dv + c0 + xc;
-            if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
-                store8(y, o);
-            } else {
+        if constexpr (OUT) {
+            // token and four columns a thread, in 256 / kThreads rounds
 #pragma unroll
-                for (int j = 0; j < 8; j++) y[j] = o[j];
+            for (int e = 0; e < 256 / kThreads; e++) {
+                const int t = (e * kThreads + tid) / 16, c = tid % 16 * 4;
+                if (t >= n) continue;
+                const float4 x4 = *reinterpret_cast<const float4*>(&sm.x[b][t][c]);
+                float4 u = make_float4(D * x4.x, D * x4.y, D * x4.z, D * x4.w);
+#pragma unroll
+                for (int l = 0; l < kL; l++) {
+                    const float4 v = *reinterpret_cast<const float4*>(&sm.part[t][l][c]);
+                    u.x += v.x;
+                    u.y += v.y;
+                    u.z += v.z;
+                    u.w += v.w;
+                }
+                float* const y = static_cast<float*>(p.y) + (t0 + t) * p.ys + (int64_t)h * p.dv + c0 + c;
+                if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
+                    *reinterpret_cast<float4*>(y) = u;
+                } else {
+                    y[0] = u.x;
+                    y[1] = u.y;
+                    y[2] = u.z;
+                    y[3] = u.w;
+                }
             }
+            __syncthreads();             // parts and x have been read
         }
     }
     float* to = nullptr;
