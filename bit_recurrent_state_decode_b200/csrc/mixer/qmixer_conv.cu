@@ -5,11 +5,11 @@
 // Bound: memory (each x read once, each y written once; 2 W + 4 operations an
 // element).  A thread owns 16 bytes of channels (eight bf16, four binary32) of a
 // walk of kWalk tokens, and has all of the walk's rows and the W - 1 in front of
-// it on their way before the first is used; a CTA holds 16 such neighbours of 8
-// walks in a row, so that the rows in front of a walk come from L1.  (A walk of
-// 16 to 64 tokens with a moving window reads less twice, but has four rows on
-// their way at a time: eight prompts of 2048 tokens by 2304 channels took 41 to
-// 53 us that way.)
+// it on their way before the first is used; a warp holds 32 such neighbours, a CTA
+// 4 walks in a row, so that the rows in front of a walk come from L1.  Eight prompts
+// of 2048 tokens by 2304 channels take 34 us (4.4 TB/s); with 16 neighbours 36, with
+// walks of 4 tokens 39 to 43, of 12 tokens 37; walks of 16 to 64 tokens with a moving
+// window and four rows on their way took 41 to 53.
 //
 // State.  Sequence s continues from state[s] and leaves its last W - 1 rows
 // there, in place.  One thread does both for its channels: the walk in which a
@@ -20,7 +20,7 @@
 
 namespace qm {
 
-constexpr int kWalk = 8, kAcross = 16, kDown = 128 / kAcross;
+constexpr int kWalk = 8, kAcross = 32, kDown = 128 / kAcross;
 
 struct ConvParams {
     const void* x;

@@ -136,6 +136,19 @@ def _span(t):
     return (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size() if t.numel() else 0
 
 
+def _pitch(t):
+    """(bytes from one row to the next, bytes of a row) of a tensor of rows with gaps;
+    None for one without."""
+    row = 1
+    for n, stride in zip(reversed(t.shape), reversed(t.stride())):
+        if n == 1:
+            continue
+        if stride != row:
+            return stride * t.element_size(), row * t.element_size()
+        row *= n
+    return None
+
+
 def _apart(fn, name, a, other, b):
     """Refuse an output that shares memory with an input; columns of one buffer's
     rows may interleave."""
@@ -144,12 +157,11 @@ def _apart(fn, name, a, other, b):
     pa, pb = a.data_ptr(), b.data_ptr()
     if pa >= pb + _span(b) or pb >= pa + _span(a):
         return
-    if a.dim() > 1 and b.dim() > 1:
-        pitch = a.stride(0) * a.element_size()
-        if pitch and pitch == b.stride(0) * b.element_size():
-            off = (pb - pa) % pitch
-            if off >= _span(a[0]) and off + _span(b[0]) <= pitch:
-                return
+    ra, rb = _pitch(a), _pitch(b)
+    if ra and rb and ra[0] == rb[0]:
+        off = (pb - pa) % ra[0]
+        if off >= ra[1] and off + rb[1] <= ra[0]:
+            return
     raise ValueError(f"{fn}: {name} overlaps {other}")
 
 
@@ -189,10 +201,11 @@ def _sequences(fn, lead, seq_starts, index):
     return seq_starts.numel() - 1, lead[0], seq_starts.data_ptr()
 
 
-def _fresh(like, shape, dtype):
-    if dtype is like.dtype and like.is_contiguous():
-        return torch.empty_like(like)
-    return like.new_empty(shape, dtype=dtype)
+def _fresh(like, dtype):
+    """A contiguous output of `like`'s shape."""
+    if dtype is like.dtype:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _given(fn, out, like, shape, dtype, inputs):
@@ -228,7 +241,7 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
 
     def body(st):
         if out is None:
-            y, ys = _fresh(x, shape, x.dtype), shape[-1]
+            y, ys = _fresh(x, x.dtype), shape[-1]
         else:
             y = _given(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
             ys = _rows(fn, "out", y, 1)
@@ -253,7 +266,7 @@ def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=
 
     def body(st):
         if out is None:
-            y, ys = _fresh(x, shape, x.dtype), shape[1]
+            y, ys = _fresh(x, x.dtype), shape[1]
         else:
             y = _given(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
             ys = _rows(fn, "out", y, 1)
@@ -274,7 +287,7 @@ def _taps(fn, x, weight, bias, state, n, index):
     if state is not None:
         sp = _dense(fn, "state", state, index, dtype, (n, width - 1, channels))
         at = x.data_ptr()       # by bounds first
-        if at < sp + state.nbytes and sp < at + x.shape[0] * x.stride(0) * 4:
+        if at < sp + state.nbytes and sp < at + x.shape[0] * max(x.stride(0), channels) * 4:
             _apart(fn, "state", state, "x", x)
     return width, weight.data_ptr(), bp, sp
 
@@ -286,22 +299,37 @@ def _selective(fn, x, dt, A, B, C, D, dt_bias):
     _tensor(fn, "x", x, None)
     code, index, xsh, dtype = _code(fn, x), x.get_device(), x.shape, x.dtype
     heads, d_v = xsh[-2], xsh[-1]
-    _tensor(fn, "dt", dt, index, None, xsh[:-1])
+    per_head = (heads,)
+    lead = xsh[:-2]
+    _tensor(fn, "dt", dt, index, None, lead + per_head)
     _tensor(fn, "B", B, index, dtype)
     bsh = B.shape
-    if len(bsh) != len(xsh) or bsh[:-2] != xsh[:-2]:
-        raise ValueError(f"{fn}: B has shape {tuple(bsh)}, expected {tuple(xsh[:-2])} + (groups, d_k)")
+    if len(bsh) != len(xsh) or bsh[:-2] != lead:
+        raise ValueError(f"{fn}: B has shape {tuple(bsh)}, expected {tuple(lead)} + (groups, d_k)")
     groups, d_k = bsh[-2], bsh[-1]
     _tensor(fn, "C", C, index, dtype, bsh)
     if groups == 0 or heads % groups:
         raise ValueError(f"{fn}: {heads} heads do not divide into {groups} groups")
-    per_head = (heads,)
-    rows = (x.data_ptr(), _rows(fn, "x", x, 2), dt.data_ptr(), _rows(fn, "dt", dt, 1),
-            _dense(fn, "A", A, index, _F32, per_head), B.data_ptr(), _rows(fn, "B", B, 2), C.data_ptr(),
-            _rows(fn, "C", C, 2))
+    rows = (x.data_ptr(), _rows2(fn, "x", x, d_v, heads * d_v), dt.data_ptr(), _rows(fn, "dt", dt, 1),
+            _dense(fn, "A", A, index, _F32, per_head), B.data_ptr(), _rows2(fn, "B", B, d_k, groups * d_k),
+            C.data_ptr(), _rows2(fn, "C", C, d_k, groups * d_k))
+    if (rows[0] | rows[5] | rows[7] | (rows[1] | rows[6] | rows[8]) * x.element_size()) & 15:
+        raise ValueError(f"{fn}: the rows of x, B and C must start on 16-byte boundaries")
     return (rows, 0 if D is None else _dense(fn, "D", D, index, _F32, per_head),
             0 if dt_bias is None else _dense(fn, "dt_bias", dt_bias, index, _F32, per_head),
             (heads, groups, d_k, d_v, code, _code(fn, dt)), index)
+
+
+def _rows2(fn, name, t, inner, row):
+    """_rows of tokens of [heads, d]: the common case first, one axis of tokens whose
+    rows are whole."""
+    s = t.stride()
+    if len(s) == 3 and s[2] == 1 and s[1] == inner:
+        if t.shape[0] <= 1:
+            return row
+        if s[0] >= row:
+            return s[0]
+    return _rows(fn, name, t, 2)
 
 
 @functools.lru_cache(maxsize=256)
@@ -351,7 +379,7 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
 
     def body(st):
         if out is None:
-            y, ys = _fresh(x, x.shape, x.dtype), sizes[0] * sizes[3]
+            y, ys = _fresh(x, x.dtype), sizes[0] * sizes[3]
         else:
             y = _given(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
             ys = _rows(fn, "out", y, 2)
@@ -377,7 +405,7 @@ def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out
 
     def body(st):
         if out is None:
-            y, ys = _fresh(x, shape, x.dtype), sizes[0] * sizes[3]
+            y, ys = _fresh(x, x.dtype), sizes[0] * sizes[3]
         else:
             y = _given(fn, out, x, shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
             ys = _rows(fn, "out", y, 2)
@@ -418,7 +446,10 @@ def load(obj, S, *, stream=None):
         _quantize(st, S.data_ptr(), codes.data_ptr(), scales.data_ptr(), 0 if ref is None else ref.data_ptr(),
                   obj.layers * obj.batch, obj.heads, obj.d_k, obj.d_v, 0 if mixed else obj.bits,
                   ctypes.addressof(hb) if mixed else 0, obj.group, obj.scale_dtype, obj.rotation)
-        obj.import_(codes, scales, ref, stream=torch.cuda.current_stream())
+        rc = Q.lib().qstate_import(obj._h, codes.data_ptr(), scales.data_ptr(),
+                                   None if ref is None else ref.data_ptr(), st)
+        if rc:
+            raise QStateError("qstate_import", rc)
     _launch(fn, S, stream, body)
 
 
@@ -441,7 +472,7 @@ def step(obj, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, out=None, 
 
     def body(st):
         if out is None:
-            y, ys = _fresh(x, x.shape, x.dtype), sizes[0] * sizes[3]
+            y, ys = _fresh(x, x.dtype), sizes[0] * sizes[3]
         else:
             y = _given(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt)))
             ys = _rows(fn, "out", y, 2)
@@ -487,6 +518,7 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
     if group and (group < 0 or columns % group):
         raise ValueError(f"{fn}: groups of {group} do not divide {columns} columns")
     x2 = _flat(fn, "x", x)
+    xs = _rows(fn, "x", x2, 1)
     before, name, other = ((BEFORE_RESIDUAL, "residual", residual) if residual is not None else
                            (BEFORE_GATE, "gate", gate) if gate is not None else (BEFORE_NONE, None, None))
     op, ostride = 0, 0
@@ -495,16 +527,15 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
         o2 = _flat(fn, name, other)
         op, ostride = o2.data_ptr(), _rows(fn, name, o2, 1)
         if before == BEFORE_RESIDUAL:
-            at, end = x2.data_ptr(), x2.shape[0] * x2.stride(0) * 4      # by bounds first
-            if at < op + o2.shape[0] * ostride * 4 and op < at + end:
+            at, reach = x2.data_ptr(), x2.shape[0] * 4                   # by bounds first
+            if at < op + o2.shape[0] * ostride * 4 and op < at + reach * xs:
                 _apart(fn, name, o2, "x", x2)
             if wp < op + o2.shape[0] * ostride * 4 and op < wp + weight.nbytes:
                 _apart(fn, name, o2, "weight", weight)
-    xs = _rows(fn, "x", x2, 1)
 
     def body(st):
         if out is None:
-            y = y2 = _fresh(x, shape, dtype or xd)
+            y = y2 = _fresh(x, dtype or xd)
             ys = columns
         else:
             y = _given(fn, out, x, shape, dtype or xd, (("x", x), (name, other), ("weight", weight)))

@@ -205,6 +205,11 @@ def test_overlaps(M):
     M._apart("f", "out", b[:, :16], "x", b[:, 16:])        # columns of one buffer's rows
     M._apart("f", "out", b, "x", torch.zeros(8, 32))
     M._apart("f", "out", b[:0], "x", b)
+    c = b.view(2, 4, 32)
+    M._apart("f", "out", c[..., :16], "x", c[..., 16:])
+    M._apart("f", "out", c[..., :16].unflatten(-1, (4, 4)), "x", c[..., 16:24])
+    with pytest.raises(ValueError):
+        M._apart("f", "out", c[..., :16], "x", c[..., 8:24])
     for other in (b, b[2:6], b[:, 15:], b.view(16, 16)):
         with pytest.raises(ValueError):
             M._apart("f", "out", b[:, :16] if other.shape[-1] == 17 else b, "x", other)
