@@ -24,7 +24,7 @@ struct NormParams {
     float* scales;
     int64_t rows;
     int columns, group;
-    float eps;
+    float eps, per_column;      // per_column = 1 / columns
     int before, out;
 };
 
@@ -104,11 +104,12 @@ __device__ __forceinline__ uint32_t largest(const f2 (&h)[4]) {
 struct Codes {
     float scale, inv;
     bool odd;            // not a number, zero, or so small that its reciprocal may overflow
-    __device__ __forceinline__ Codes(uint32_t most, float qmax) {
+    // `unit`: 1 / Qmax.  (A scale one unit off its quotient stands for the same values.)
+    __device__ __forceinline__ Codes(uint32_t most, float unit) {
         const bool bad = most >= 0x7f800000u;
-        scale = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(most), qmax);
+        scale = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(most) * unit;
         odd = !(scale >= 1e-36f);
-        inv = __frcp_rn(scale);
+        inv = rcp_approx(scale);
     }
     __device__ __forceinline__ void divide(const f2 (&y)[4], float (&z)[8]) const {
         f2 q[4];
@@ -142,7 +143,7 @@ struct Codes {
 };
 
 template <class T, bool VEC, int BEFORE, int THREADS, int N>
-__global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS == 128 && N <= 2 ? 12 : 1) norm_kernel(const NormParams p) {
     constexpr int kBlock = THREADS < 128 ? 128 : THREADS;
     constexpr int kWarps = THREADS / 32;
     __shared__ float sums[kWarps];
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
 #pragma unroll
         for (int i = 0; i < kWarps; i++) sum += sums[i];
     }
-    const float r = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, (float)p.columns) + p.eps));
+    const float r = rsqrtf(fmaf(sum, p.per_column, p.eps));         // 2 units of binary32
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
         return;
     }
     uint8_t* const y = static_cast<uint8_t*>(p.y) + row * p.ys;
-    const float qmax = p.out == QMIXER_OUT_INT8 ? 127.0f : 448.0f;
+    const float unit = p.out == QMIXER_OUT_INT8 ? 1.0f / 127.0f : 1.0f / 448.0f;
     if (!p.group) {
         most = __reduce_max_sync(~0u, most);
         if constexpr (THREADS > 32) {
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS) norm_kernel(con
             for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
         }
         if (left <= 0) continue;
-        const Codes q(m, qmax);
+        const Codes q(m, unit);
         if (p.group ? (c & (p.group - 1)) == 0 : c == 0)
             p.scales[row * ngroups + (p.group ? c / p.group : 0)] = q.scale;
         const uint2 b = p.out == QMIXER_OUT_INT8 ? q.int8(h[i]) : q.e4m3(h[i]);
@@ -303,7 +304,7 @@ extern "C" int qmixer_norm(const qmixer_norm_args* args, qstate_stream stream) {
     if (!a.rows) return QSTATE_OK;
     if (!a.x || !a.weight || !a.y || (a.before && !a.other) || (a.out && !a.scales)) return QSTATE_EINVAL;
     const qm::NormParams p{a.x, a.x_stride, a.other, a.other_stride, a.weight, a.y, a.y_stride, a.scales,
-                           a.rows, a.columns, a.group, a.eps, a.before, a.out};
+                           a.rows, a.columns, a.group, a.eps, 1.0f / (float)a.columns, a.before, a.out};
     // eight a.columns at a time where a.columns, strides and bases allow 16-byte
     // accesses (8-byte ones of codes); else element by element
     const int unit = 16 / size;
