@@ -3,12 +3,15 @@
 // y rounded once on the way out: to the inputs' type, or to 8-bit codes with a
 // binary32 scale per row or per group of columns.
 //
-// Bound: memory (x and the second operand read once, y written once).  kThreads
-// threads hold one row in registers between the sum of squares and the output,
-// so nothing is read twice; each thread takes eight consecutive columns at a
-// time, kThreads * 8 columns apart, all loads of a row in flight together.  The
-// groups of the 8-bit scales are powers of two of at most 256 columns: 32 lanes
-// or fewer of one warp, joined by shuffles.
+// Bound: memory (x and the second operand read once, y written once).  A warp, 128
+// or 512 threads hold one row in registers between the sum of squares and the
+// output, so nothing is read twice; each thread takes eight consecutive columns at a
+// time, all loads of a row in flight together.  The groups of the 8-bit scales are
+// powers of two of at most 256 columns: 32 lanes or fewer of one warp, joined by
+// shuffles.  Measured on 16384 rows of 2048 bfloat16: residual, output in type 42 us
+// (6.3 TB/s, 97% of the copy rate); gate to e4m3 in groups of 128 40 us (4.2 TB/s) and
+// int8 of whole rows 27 us (3.7 TB/s), both bound by instruction issue (77% of the
+// slots): what a code costs beside its bytes.
 #include "qmixer_common.cuh"
 
 namespace qm {
@@ -263,7 +266,8 @@ template <class T, bool VEC, int BEFORE, int THREADS, int N> void launch_norm(co
 }
 
 // Up to 1024 columns in a warp of its own where there are rows enough to fill the
-// SMs, else 128 threads a row; beyond 4096 columns 512.
+// SMs, else 128 threads a row (2048 columns in a warp took 84 us where 128 threads
+// take 45); beyond 4096 columns 512.
 template <class T, bool VEC, int BEFORE> void by_columns(const NormParams& p, cudaStream_t st) {
     const int v = (p.columns + 7) / 8;
     const bool few = p.rows < 148 * 8;

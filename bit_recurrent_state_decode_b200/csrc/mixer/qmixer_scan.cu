@@ -75,7 +75,7 @@ int sm_count() {
 ScanPlan scan_plan(int sequences, int64_t tokens, int heads, int dk, int dv, int dtype, bool ragged, int sms) {
     const bool chunked = dtype == QSTATE_BF16;
     const int64_t unit = chunked ? kChunk : kBatchTokens;
-    const int64_t chains = (int64_t)heads * (dv / 64), resident = (chunked ? 1 : dk == 64 ? 4 : 2) * (int64_t)sms;
+    const int64_t chains = (int64_t)heads * (dv / 64), resident = (chunked ? 1 : dk == 64 ? 3 : 2) * (int64_t)sms;
     const double states = chunked ? 0.41 : 0.6, launches = chunked ? 4 * kChunk : 2 * kBatchTokens;
     const int64_t start = chunked ? 0 : kBatchTokens;
     const int64_t mean = tokens / sequences, longest = ragged ? (4 * mean < tokens ? 4 * mean : tokens) : mean;

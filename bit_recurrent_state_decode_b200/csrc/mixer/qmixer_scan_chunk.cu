@@ -38,6 +38,13 @@
 // twice, by rows for G and by columns (transposed descriptor) for B^T.  Loops are
 // unrolled no further than they have to be: the roles share the instruction cache,
 // and with all of it unrolled a chunk took twice as long.
+//
+// Measured: eight sequences of 2048 tokens, 32 heads of 128 x 64, 88 us, 4000 cycles a
+// chunk and SM.  The products take 2100 of them (48 cycles each at 64 columns, 64 at
+// 128: operand reads from shared memory), instructions issue in half of the slots;
+// what bounds a chunk is the chain S, C S, third part, increment, S, with two waits
+// for tensor memory and two for shared memory on it, and 256 chains on 148 SMs take
+// two rounds.  All warps in step, two CTAs an SM, took 137 us.
 #include <cuda.h>
 
 #include "qmixer_scan.cuh"
@@ -619,7 +626,8 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
 #pragma unroll
             for (int u = 0; u < 3; u++)
                 if (u < quad) f *= sc.block[u];
-            if (!wait(B_Y, c)) break;
+            // (the first two have passed; X is read here, as they left it)
+            if (!wait2(B_FULL, c) || !wait2(B_W01, c) || !wait(B_Y, c)) break;
             tc_after();
             const unsigned char* const xs = sm + (c & 1) * L::kStage + L::kXs;
             const int64_t t = seg.from + (int64_t)c * kChunk + row;
