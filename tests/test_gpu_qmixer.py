@@ -711,3 +711,114 @@ def test_a_token_captured_and_replayed():
         obj.close()
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- wider calls
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_scan_many_sequences_cut_unevenly(dtype):
+    """More sequences than a warp counts at once, one of them long enough to be cut."""
+    g = gen(90)
+    lens = [3, 0, 17, 4000, 1] + [5 + i % 9 for i in range(72)]
+    starts = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    n, T = len(lens), starts[-1]
+    x, dt, A, B, C, D, bias = selective(g, T, 1, 1, 64, 64, dtype)
+    st = normal(g, n, 1, 64, 64)
+    want = scan_exact(x, dt, A, B, C, D, bias, True, st, starts)
+    y = M.scan(x, dt, A, B, C, D, dt_bias=bias, state=st, initial=True, seq_starts=ints(starts))
+    check_scan(y, st, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_scan_equal_sequences_cut(dtype):
+    g = gen(91)
+    n, L = 3, 1900
+    x, dt, A, B, C, D, bias = selective(g, n * L, 2, 1, 128, 64, dtype)
+    st = normal(g, n, 2, 128, 64)
+    want = scan_exact(x, dt, A, B, C, D, bias, True, st, [0, L, 2 * L, 3 * L])
+    by = [t.view(n, L, *t.shape[1:]) for t in (x, dt, B, C)]
+    y = M.scan(by[0], by[1], A, by[2], by[3], D, dt_bias=bias, state=st, initial=True)
+    check_scan(y.view(n * L, 2, 64), st, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_outputs_at_any_alignment(dtype):
+    """Outputs that are views at odd columns of wider buffers, the columns beside
+    them left as they were."""
+    g = gen(92)
+    T, H, N, P = 200, 2, 64, 64
+    x, dt, A, B, C, D, bias = selective(g, T, H, 1, N, P, dtype)
+    st = normal(g, T, H, N, P)
+    for off in (1, 8, 16):
+        wide = torch.full((T, 160), 3.0, dtype=dtype, device=DEV)
+        out = wide[:, off:off + H * P].unflatten(-1, (H, P))
+        assert torch.equal(M.scan(x, dt, A, B, C, D, dt_bias=bias, out=out), M.scan(x, dt, A, B, C, D, dt_bias=bias))
+        assert bool((wide[:, :off] == 3).all()) and bool((wide[:, off + H * P:] == 3).all())
+        M.scan_step(x, dt, A, B, C, D, dt_bias=bias, state=st.clone(), out=out)
+        assert torch.equal(out, M.scan_step(x, dt, A, B, C, D, dt_bias=bias, state=st.clone()))
+        u, w = normal(g, 9, 64).to(dtype), torch.ones(64, dtype=dtype, device=DEV)
+        for to in (torch.int8, torch.float8_e4m3fn):
+            codes = torch.zeros(9, 100, dtype=torch.uint8, device=DEV).view(to)
+            M.norm(u, w, dtype=to, group=16, out=codes[:, off:off + 64])
+            assert torch.equal(codes[:, off:off + 64].float(), M.norm(u, w, dtype=to, group=16)[0].float())
+            codes[:, off:off + 64] = 0
+            assert not bool(codes.float().any())
+
+
+def test_offsets_past_32_bits():
+    """Rows that lie further apart than 2^31 elements in all."""
+    T, pitch = 70000, 32768
+    wide = torch.empty(T, pitch, dtype=BF, device=DEV)               # 4.6 GB
+    g = gen(93)
+    x, dt, A, B, C, D, bias = selective(g, T, 1, 1, 64, 64, BF)
+    cols = [wide[:, 64 * i:64 * i + 64] for i in range(4)]
+    for c, t in zip(cols, (x, B, C)):
+        c.copy_(t.view(T, 64))
+    xv, Bv, Cv = (c.unflatten(-1, (1, 64)) for c in cols[:3])
+    out = cols[3].unflatten(-1, (1, 64))
+    M.scan(xv, dt, A, Bv, Cv, D, dt_bias=bias, out=out)
+    assert torch.equal(out, M.scan(x, dt, A, B, C, D, dt_bias=bias))
+    M.scan_step(xv, dt, A, Bv, Cv, D, dt_bias=bias, state=torch.zeros(T, 1, 64, 64, device=DEV), out=out)
+    assert torch.equal(out, M.scan_step(x, dt, A, B, C, D, dt_bias=bias, state=torch.zeros(T, 1, 64, 64, device=DEV)))
+    w = normal(g, 64, 4).to(BF)
+    M.conv(cols[0], w, out=cols[3])
+    assert torch.equal(cols[3], M.conv(x.view(T, 64), w))
+    M.norm(cols[0], torch.ones(64, dtype=BF, device=DEV), gate=cols[1], out=cols[3])
+    assert torch.equal(cols[3], M.norm(x.view(T, 64), torch.ones(64, dtype=BF, device=DEV), gate=B.view(T, 64)))
+
+
+def test_scans_and_products_side_by_side():
+    """Full scans on two streams beside matrix products on a third, which use the
+    same tensor memory: all end, with the results they have alone."""
+    sets = [selective(gen(94 + i), 2000, 32, 1, 128, 64, BF) for i in range(2)]
+    a = normal(gen(96), 4096, 4096).to(BF)
+    want = [M.scan(x, dt, A, B, C, D, dt_bias=bias) for x, dt, A, B, C, D, bias in sets]
+    product = a @ a
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for _ in range(6):
+        for (x, dt, A, B, C, D, bias), s in zip(sets, streams):
+            outs.append(M.scan(x, dt, A, B, C, D, dt_bias=bias, stream=s))
+        with torch.cuda.stream(streams[2]):
+            p = a @ a
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, want[i % 2])
+    assert torch.equal(p, product)
+
+
+def test_conv_step_captured_and_replayed():
+    """Captured once and replayed: the states move on each time."""
+    g = gen(97)
+    x, w = normal(g, 4, 64).to(BF), normal(g, 64, 4).to(BF)
+    a = torch.zeros(4, 3, 64, dtype=BF, device=DEV)
+    b = a.clone()
+    M.conv_step(x, w, state=a)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        y = M.conv_step(x, w, state=a)
+    gr.replay()
+    gr.replay()
+    for _ in range(3):
+        want = M.conv_step(x, w, state=b)
+    assert torch.equal(y, want) and torch.equal(a, b)
