@@ -298,26 +298,45 @@ def _selective(fn, x, dt, A, B, C, D, dt_bias):
     heads, groups, d_k, d_v) and the device."""
     _tensor(fn, "x", x, None)
     code, index, xsh, dtype = _code(fn, x), x.get_device(), x.shape, x.dtype
-    heads, d_v = xsh[-2], xsh[-1]
+    lead, heads, d_v = xsh[:-2], xsh[-2], xsh[-1]
     per_head = (heads,)
-    lead = xsh[:-2]
-    _tensor(fn, "dt", dt, index, None, lead + per_head)
     _tensor(fn, "B", B, index, dtype)
     bsh = B.shape
     if len(bsh) != len(xsh) or bsh[:-2] != lead:
         raise ValueError(f"{fn}: B has shape {tuple(bsh)}, expected {tuple(lead)} + (groups, d_k)")
     groups, d_k = bsh[-2], bsh[-1]
-    _tensor(fn, "C", C, index, dtype, bsh)
     if groups == 0 or heads % groups:
         raise ValueError(f"{fn}: {heads} heads do not divide into {groups} groups")
-    rows = (x.data_ptr(), _rows2(fn, "x", x, d_v, heads * d_v), dt.data_ptr(), _rows(fn, "dt", dt, 1),
-            _dense(fn, "A", A, index, _F32, per_head), B.data_ptr(), _rows2(fn, "B", B, d_k, groups * d_k),
-            C.data_ptr(), _rows2(fn, "C", C, d_k, groups * d_k))
+    if not _usual(index, dtype, C, bsh, dt, lead + per_head, A, D, dt_bias, per_head):
+        # one of them is refused, or unusual: each by itself
+        _tensor(fn, "dt", dt, index, None, lead + per_head)
+        _tensor(fn, "C", C, index, dtype, bsh)
+        for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
+            if t is not None or name == "A":
+                _dense(fn, name, t, index, _F32, per_head)
+    rows = (x.data_ptr(), _rows2(fn, "x", x, d_v, heads * d_v), dt.data_ptr(), _rows(fn, "dt", dt, 1), A.data_ptr(),
+            B.data_ptr(), _rows2(fn, "B", B, d_k, groups * d_k), C.data_ptr(), _rows2(fn, "C", C, d_k, groups * d_k))
     if (rows[0] | rows[5] | rows[7] | (rows[1] | rows[6] | rows[8]) * x.element_size()) & 15:
         raise ValueError(f"{fn}: the rows of x, B and C must start on 16-byte boundaries")
-    return (rows, 0 if D is None else _dense(fn, "D", D, index, _F32, per_head),
-            0 if dt_bias is None else _dense(fn, "dt_bias", dt_bias, index, _F32, per_head),
+    return (rows, 0 if D is None else D.data_ptr(), 0 if dt_bias is None else dt_bias.data_ptr(),
             (heads, groups, d_k, d_v, code, _code(fn, dt)), index)
+
+
+def _usual(index, dtype, C, csh, dt, dsh, A, D, dt_bias, per_head):
+    """Whether the checks of _selective hold for these, without their messages."""
+    try:
+        if not (C.get_device() == dt.get_device() == A.get_device() == index and C.dtype is dtype and A.dtype is _F32
+                and C.shape == csh and dt.shape == dsh and A.shape == per_head and A.is_contiguous()):
+            return False
+        grad = C.requires_grad or dt.requires_grad or A.requires_grad
+        for t in (D, dt_bias):
+            if t is not None:
+                if not (t.get_device() == index and t.dtype is _F32 and t.shape == per_head and t.is_contiguous()):
+                    return False
+                grad = grad or t.requires_grad
+        return not (grad and torch.is_grad_enabled())
+    except AttributeError:      # not a tensor
+        return False
 
 
 def _rows2(fn, name, t, inner, row):
@@ -438,16 +457,16 @@ def load(obj, S, *, stream=None):
 
     def body(st):
         # an object's own buffers are reached by qstate_import alone
-        codes = S.new_empty(z["code_bytes"], dtype=torch.uint8)
-        scales = S.new_empty(max(z["scale_bytes"], 4), dtype=torch.uint8)
+        at = (z["code_bytes"] + 255) // 256 * 256
+        codes = torch.empty(at + z["scale_bytes"], dtype=torch.uint8, device=S.device)
+        cp, scales = codes.data_ptr(), codes.data_ptr() + at
         ref = torch.empty_like(S) if z["ref_bytes"] else None
         mixed = obj.head_bits is not None
         hb = (ctypes.c_uint8 * obj.heads)(*obj.head_bits) if mixed else None
-        _quantize(st, S.data_ptr(), codes.data_ptr(), scales.data_ptr(), 0 if ref is None else ref.data_ptr(),
+        _quantize(st, S.data_ptr(), cp, scales, 0 if ref is None else ref.data_ptr(),
                   obj.layers * obj.batch, obj.heads, obj.d_k, obj.d_v, 0 if mixed else obj.bits,
                   ctypes.addressof(hb) if mixed else 0, obj.group, obj.scale_dtype, obj.rotation)
-        rc = Q.lib().qstate_import(obj._h, codes.data_ptr(), scales.data_ptr(),
-                                   None if ref is None else ref.data_ptr(), st)
+        rc = Q.lib().qstate_import(obj._h, cp, scales, None if ref is None else ref.data_ptr(), st)
         if rc:
             raise QStateError("qstate_import", rc)
     _launch(fn, S, stream, body)
