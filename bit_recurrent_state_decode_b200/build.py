@@ -3,7 +3,8 @@
     python -m bit_recurrent_state_decode_b200.build [--force] [-v]
 
 libqstate.so (csrc/) is the quantized recurrent-state step, libqmixer.so
-(csrc/mixer/) the operators around it.  Each .cu unit is compiled in parallel,
+(csrc/mixer/) the operators around it, and _qmixer_usual.so (csrc/mixer/binding/) the
+module that makes their usual calls from Python.  Each .cu unit is compiled in parallel,
 then each library is linked with a static CUDA runtime; a library whose
 sources are older than it is left alone.  No fast-math: the step's arithmetic
 is specified to the bit (see include/qstate.h), so FMA contraction is disabled
@@ -33,6 +34,9 @@ CFLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", 
 # library -> folder of its units, public headers
 LIBS = {LIB: (CSRC, ("qstate.h",)), MIXER_LIB: (os.path.join(CSRC, "mixer"), ("qstate.h", "qmixer.h"))}
 
+USUAL = os.path.join(PKG, "_qmixer_usual.so")
+USUAL_SRC = os.path.join(CSRC, "mixer", "binding", "qmixer_usual.cpp")
+
 
 def _deps(lib):
     src, headers = LIBS[lib]
@@ -47,13 +51,38 @@ def _lib_up_to_date(lib) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps(lib))
 
 
+def _usual_up_to_date() -> bool:
+    return os.path.exists(USUAL) and all(
+        os.path.getmtime(d) <= os.path.getmtime(USUAL)
+        for d in (USUAL_SRC, os.path.join(ROOT, "include", "qmixer.h"), __file__))
+
+
 def up_to_date() -> bool:
-    return all(_lib_up_to_date(lib) for lib in LIBS)
+    return all(_lib_up_to_date(lib) for lib in LIBS) and _usual_up_to_date()
+
+
+def _build_usual():
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    tmp = USUAL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-o", tmp, USUAL_SRC,
+           "-I" + os.path.join(ROOT, "include"), "-I" + sysconfig.get_paths()["include"],
+           "-I/usr/local/cuda/include"]
+    cmd += ["-isystem" + d for d in cpp_extension.include_paths()]
+    cmd += [f for d in cpp_extension.library_paths() for f in ("-L" + d, "-Wl,-rpath," + d)]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-L" + PKG, "-lqmixer", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the compiler failed on {USUAL_SRC}:\n{r.stderr}")
+    os.replace(tmp, USUAL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     stale = [lib for lib in LIBS if force or not _lib_up_to_date(lib)]
     if not stale:
+        if force or not _usual_up_to_date():
+            _build_usual()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose else []
@@ -80,6 +109,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if r.returncode != 0:
                 raise RuntimeError(f"link failed:\n{r.stderr}")
             os.replace(tmp, lib)
+    _build_usual()
     return LIB
 
 

@@ -8,7 +8,8 @@ operators around the recurrent state of a Mamba2 layer.
     norm                 root-mean-square norm, with a residual or a gate, and 8-bit output
 
 Argument checks and marshalling only: the arithmetic runs in the CUDA kernels
-of the library.  Calls are asynchronous on the current stream of the tensors'
+of the library.  A usual call (its own output, the current stream) is checked and
+launched by the compiled module _qmixer_usual; what that leaves takes the way below.  Calls are asynchronous on the current stream of the tensors'
 device, or on `stream`; tensors of another stream have to be ordered before
 the call by the caller, as for any PyTorch operator.  The library must have
 been built; there is no CPU fallback and no autograd: inputs that require a
@@ -42,6 +43,24 @@ _FIELDS = {"qmixer_conv": "PqPPPPqPiqiiii", "qmixer_conv_step": "PqPPPPqiiiii",
 EXPORTS = tuple(_FIELDS) + ("qmixer_scan_workspace",)
 
 _lib = None
+
+
+class _Load:
+    """Stands for _qmixer_usual until the first call of one of its functions."""
+
+    def __getattr__(self, name):
+        global _usual
+        from . import build
+        lib()
+        if not os.path.exists(build.USUAL):
+            raise RuntimeError(f"{build.USUAL} is missing: build it with "
+                               "`python -m bit_recurrent_state_decode_b200.build`")
+        from . import _qmixer_usual
+        _usual = _qmixer_usual
+        return getattr(_usual, name)
+
+
+_usual = _Load()
 
 
 def lib():
@@ -228,6 +247,10 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
     its row with initial=True, else from zeros, and leaves its last rows there.
     Tokens behind the last sequence stay as they are in `out` (undefined where
     `out` is not given).  Returns out, shaped like x."""
+    if out is None and stream is None:
+        y = _usual.conv(x, weight, bias, state, bool(activation), bool(initial), seq_starts)
+        if y is not None:
+            return y
     fn = "conv"
     _tensor(fn, "x", x, None)
     if x.dim() not in (2, 3):
@@ -254,6 +277,10 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
 def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=None):
     """The same for one token of each sequence: x [batch, channels]; state
     [batch, width - 1, channels] moves on by one token."""
+    if out is None and stream is None:
+        y = _usual.conv_step(x, weight, bias, state, bool(activation))
+        if y is not None:
+            return y
     fn = "conv_step"
     _tensor(fn, "x", x, None)
     if x.dim() != 2:
@@ -307,7 +334,7 @@ def _selective(fn, x, dt, A, B, C, D, dt_bias):
     groups, d_k = bsh[-2], bsh[-1]
     if groups == 0 or heads % groups:
         raise ValueError(f"{fn}: {heads} heads do not divide into {groups} groups")
-    if not _usual(index, dtype, C, bsh, dt, lead + per_head, A, D, dt_bias, per_head):
+    if not _operands_hold(index, dtype, C, bsh, dt, lead + per_head, A, D, dt_bias, per_head):
         # one of them is refused, or unusual: each by itself
         _tensor(fn, "dt", dt, index, None, lead + per_head)
         _tensor(fn, "C", C, index, dtype, bsh)
@@ -322,7 +349,7 @@ def _selective(fn, x, dt, A, B, C, D, dt_bias):
             (heads, groups, d_k, d_v, code, _code(fn, dt)), index)
 
 
-def _usual(index, dtype, C, csh, dt, dsh, A, D, dt_bias, per_head):
+def _operands_hold(index, dtype, C, csh, dt, dsh, A, D, dt_bias, per_head):
     """Whether the checks of _selective hold for these, without their messages."""
     try:
         if not (C.get_device() == dt.get_device() == A.get_device() == index and C.dtype is dtype and A.dtype is _F32
@@ -383,6 +410,10 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
     there.  Rows may be views into wider ones, on 16-byte boundaries.  Tokens
     behind the last sequence stay as they are in `out` (undefined where `out`
     is not given).  Returns out, shaped like x."""
+    if out is None and stream is None:
+        y = _usual.scan(x, dt, A, B, C, D, dt_bias, state, bool(softplus), bool(initial), seq_starts)
+        if y is not None:
+            return y
     fn = "scan"
     if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError(f"{fn}: x must be [batch, length, heads, d_v] or [tokens, heads, d_v]")
@@ -413,6 +444,10 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
 def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out=None, stream=None):
     """The same for one token of each sequence: x [batch, heads, d_v]; state
     [batch, heads, d_k, d_v] float32 moves on by one token."""
+    if out is None and stream is None:
+        y = _usual.scan_step(x, dt, A, B, C, D, dt_bias, state, bool(softplus))
+        if y is not None:
+            return y
     fn = "scan_step"
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{fn}: x must be [batch, heads, d_v]")
@@ -520,6 +555,13 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
     scales, with float32 scales [.., columns / group] of `group` consecutive
     columns (a power of two from 8 to 256), or [.., 1] of whole rows for 0; a
     row or group without a finite maximum gets the scale NaN."""
+    kind = _OUT.get(dtype)
+    if out is None and stream is None and scales is None and kind is not None and (residual is None or gate is None):
+        y = _usual.norm(x, weight, residual if gate is None else gate,
+                        BEFORE_RESIDUAL if residual is not None else BEFORE_GATE if gate is not None else BEFORE_NONE,
+                        eps, kind, group)
+        if y is not None:
+            return y
     fn = "norm"
     _tensor(fn, "x", x, None)
     code, index, shape, xd = _code(fn, x), x.get_device(), x.shape, x.dtype
@@ -529,7 +571,6 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
     wp = _dense(fn, "weight", weight, index, xd, (columns,))
     if residual is not None and gate is not None:
         raise ValueError(f"{fn}: residual or gate, not both")
-    kind = _OUT.get(dtype)
     if kind is None:
         raise ValueError(f"{fn}: dtype {dtype} is not None, torch.int8 or torch.float8_e4m3fn")
     if kind == OUT_SAME and (group or scales is not None):

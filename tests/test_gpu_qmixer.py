@@ -822,3 +822,80 @@ def test_conv_step_captured_and_replayed():
     for _ in range(3):
         want = M.conv_step(x, w, state=b)
     assert torch.equal(y, want) and torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- the compiled calls
+def test_usual_calls_are_the_python_ones(monkeypatch):
+    """Each operator's usual call is answered by the compiled module, and with it out
+    of the way the Python checks give the same bits."""
+    g = gen(98)
+    x, dt, A, B, C, D, bias = selective(g, 150, 4, 2, 64, 128, BF, view=True)
+    st = normal(g, 150, 4, 64, 128)
+    one, cs = normal(g, 1, 4, 64, 128), normal(g, 2, 3, 64).to(BF)
+    u, w = normal(g, 2, 64).to(BF), normal(g, 64, 4).to(BF)
+    by = lambda t: t.view(3, 50, *t.shape[1:])  # noqa: E731
+    calls = {
+        "scan_step": lambda: [M.scan_step(x, dt, A, B, C, D, dt_bias=bias, state=(s := st.clone())), s],
+        "scan": lambda: [M.scan(x, dt, A, B, C, D, dt_bias=bias, state=(s := one.clone()), initial=True), s,
+                         M.scan(x, dt, A, B, C, seq_starts=ints([0, 20, 150])),
+                         M.scan(by(x.contiguous()), by(dt), A, by(B.contiguous()), by(C.contiguous()), softplus=False)],
+        "conv_step": lambda: [M.conv_step(u, w, w[:, 0].contiguous(), state=(s := cs.clone())), s],
+        "conv": lambda: [M.conv(x.flatten(1), w.repeat(8, 1), seq_starts=ints([0, 20, 150])),
+                         M.conv(u[None], w, state=(s := cs[:1].clone()), initial=True, activation=False), s],
+        "norm": lambda: [*M.norm(u, w[:, 0].contiguous(), gate=u, dtype=torch.int8, group=16),
+                         M.norm(x.flatten(1), torch.ones(512, dtype=BF, device=DEV)),
+                         M.norm(u, w[:, 0].contiguous(), residual=(r := u.clone()), eps=1e-3), r],
+    }
+    M.norm(u, w[:, 0].contiguous())
+    import types
+    names = ("conv", "conv_step", "scan", "scan_step", "norm")
+    real = M._usual
+    for name, call in calls.items():
+        seen = []
+
+        def spy(*a, _f=getattr(real, name)):
+            seen.append(_f(*a))
+            return seen[-1]
+        monkeypatch.setattr(M, "_usual", types.SimpleNamespace(**{n: spy if n == name else getattr(real, n) for n in names}))
+        got = call()
+        assert seen and all(s is not None for s in seen), name
+        monkeypatch.setattr(M, "_usual", types.SimpleNamespace(**{n: lambda *a: None for n in names}))
+        for a, b in zip(got, call()):
+            assert a.dtype == b.dtype and a.shape == b.shape, name
+            a, b = a.float(), b.float()         # (time steps below zero grow until they overflow)
+            assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(), b.nan_to_num()), name
+        monkeypatch.setattr(M, "_usual", real)
+
+
+def test_compiled_calls_leave_the_rest_to_python():
+    u = M._usual
+    x = torch.zeros(4, 2, 64, dtype=BF, device=DEV)
+    dt, A = torch.zeros(4, 2, device=DEV), torch.zeros(2, device=DEV)
+    st = torch.zeros(4, 2, 64, 64, device=DEV)
+    good = [x, dt, A, x, x, None, None, st, True]
+    assert u.scan_step(*good) is not None
+    for i, bad in ((0, None), (0, 3), (0, x.cpu()), (0, x.float()), (0, x.half()), (0, x[:3]), (0, x.transpose(0, 1)),
+                   (0, torch.zeros(4, 2, 72, dtype=BF, device=DEV)[..., 1:65]), (1, dt[:, :1]), (1, dt.double()),
+                   (2, A.double()), (2, None), (2, A[:1]), (3, x[..., :32]), (4, x[:, :1]), (5, A.cpu()), (6, dt[0, :1]),
+                   (7, None), (7, st[:3]), (7, st.double()), (7, st.transpose(2, 3)),
+                   (0, torch.zeros(4, 2, 64, dtype=BF, device=DEV, requires_grad=True))):
+        assert u.scan_step(*good[:i], bad, *good[i + 1:]) is None, i
+    assert u.scan_step(*good[:8]) is None and u.scan_step() is None
+    with torch.no_grad():
+        assert u.scan_step(torch.zeros(4, 2, 64, dtype=BF, device=DEV, requires_grad=True), *good[1:]) is not None
+    # an output that would lie in an input: the state inside x
+    both = torch.zeros(4 * 2 * 64 * 64, device=DEV)
+    assert u.scan_step(both[:512].view(4, 2, 64), dt, A, both[:512].view(4, 2, 64), both[512:1024].view(4, 2, 64), None,
+                       None, both.view(4, 2, 64, 64), True) is None
+    c, w = torch.zeros(4, 64, dtype=BF, device=DEV), torch.zeros(64, 4, dtype=BF, device=DEV)
+    s = torch.zeros(4, 3, 64, dtype=BF, device=DEV)
+    assert u.conv_step(c, w, None, s, True) is not None
+    for a in ((c, w[:, :3], None, s, True), (c, w, w[:, 0], s, True), (c, w, None, s[:3], True), (c, w, None, None, True),
+              (c, w.float(), None, s, True), (c[:, :32], w, None, s, True)):
+        assert u.conv_step(*a) is None
+    assert u.conv(c, w, None, None, True, True, None) is None                       # nothing to continue from
+    assert u.conv(c, w, None, None, True, False, torch.tensor([0, 4])) is None       # starts on the host
+    n = torch.zeros(64, dtype=BF, device=DEV)
+    for a in ((c, n, c, 1, 1e-5, 0, 0), (c, n, c[:2], 2, 1e-5, 0, 0), (c, n, None, 0, 1e-5, 1, 48),
+              (c, n[:32], None, 0, 1e-5, 0, 0), (c, n, None, 0, "a", 0, 0), (c, n, None, 0, -1.0, 0, 0)):
+        assert u.norm(*a) is None
