@@ -5,30 +5,40 @@
 // A CTA takes 64 value columns of one head over one segment, with the state in
 // registers: a thread holds 8 rows x 4 columns as pairs of rows, so that B and C
 // come from shared memory as the pairs that the packed binary32 instructions take
-// (sm_100 issues two operations of a pair at once).  A token costs 48 packed
-// instructions and five 16-byte shared loads a thread: instruction issue is the
-// bound, not memory.  kBatch tokens are staged at a time while the next ones are on
+// (sm_100 issues two operations of a pair at once).  Inside a batch of kBatch tokens
+// the state is kept divided by c_t, the product of the batch's decays up to t:
+//   S_t / c_t = S_{t-1} / c_{t-1} + (dt x / c_t) B^T,  y = c_t (S_t / c_t)^T C + D x
+// which spares the decay's multiplication of every element (a third of the
+// instructions), as long as every c_t lies in 2^-40 .. 2^40; from the first token on
+// that leaves it, the batch takes the plain form.  A token then costs 32 packed instructions and five
+// 16-byte shared loads a thread: instruction issue is the bound, not memory.  kBatch tokens are staged at a time while the next ones are on
 // their way to registers.  The 8 or 16 threads of a column leave their parts of y in
 // shared memory, where they are added once per batch (shuffles within the token
 // took a fifth of the instructions and most of the waiting).  Eight sequences of 1024
-// tokens, 32 heads of 128 x 64, take 367 us; the packed instructions alone would take
-// 180, issuing every other cycle.
+// tokens, 32 heads of 128 x 64, take 333 us (367 with the decay in every token); the
+// packed instructions alone would take 120, issuing every other cycle.
+#include <type_traits>
+
 #include "qmixer_scan.cuh"
 
 namespace qm {
 
 constexpr int kBatch = kBatchTokens;
+constexpr float kLeast = 0x1p-40f;
 
 template <int N, bool OUT> struct RecSmem {
     static constexpr int kOut = OUT ? kBatch : 1;
-    float k[2][kBatch][N], x[2][kBatch][64];
-    float2 ad[2][kBatch];        // decay, time step
-    float q[2][kOut][N];
-    float part[kOut][N / 8][68];     // a row of 64 shifted by four banks against the next
+    // all but the last are read 16 bytes at a time
+    alignas(16) float k[2][kBatch][N];
+    alignas(16) float x[2][kBatch][64];
+    alignas(16) float q[2][kOut][N];
+    alignas(16) float part[kOut][N / 8][68];     // a row of 64 shifted by four banks against the next
+    alignas(16) float2 ad[2][kBatch];            // decay and time step, or their scaled forms
+    int scaled[2];               // so many leading tokens in the scaled form
 };
 
 template <int N, bool OUT>
-__global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const ScanParams p) {
     constexpr int kThreads = N * 2, kL = N / 8;      // threads of one column group
     extern __shared__ __align__(16) unsigned char raw[];
     RecSmem<N, OUT>& sm = *reinterpret_cast<RecSmem<N, OUT>*>(raw);
@@ -83,7 +93,21 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
         store8(&sm.k[b][kr][kc], nk);
         if (OUT) store8(&sm.q[b][kr][kc], nq);
         if (tid < 128) store8(&sm.x[b][xr][xc], nx);
-        if (tid < kBatch) sm.ad[b][tid] = make_float2(na, nd);
+        if (tid < 32) {
+            // c_t, the product of the batch's decays up to token t
+            float c = na;
+#pragma unroll
+            for (int d = 1; d < kBatch; d <<= 1) {
+                const float u = __shfl_up_sync(~0u, c, d);
+                if (tid >= d) c *= u;
+            }
+            const bool fits = c >= kLeast && c <= 1.0f / kLeast;
+            // the tokens in front of the first that leaves the range: whatever a later
+            // token holds, an earlier one is computed alike
+            const int first = __ffs(__ballot_sync(~0u, !fits || tid >= kBatch)) - 1;
+            if (tid < kBatch) sm.ad[b][tid] = tid < first ? make_float2(c, __fdiv_rn(nd, c)) : make_float2(na, nd);
+            if (tid == 0) sm.scaled[b] = first;
+        }
     };
 
     float total = 1.0f;
@@ -94,8 +118,9 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
     for (int64_t t0 = seg.from; t0 < seg.to; t0 += kBatch, b ^= 1) {
         fetch(t0 + kBatch);
         const int n = seg.to - t0 < kBatch ? (int)(seg.to - t0) : kBatch;
-#pragma unroll 4
-        for (int t = 0; t < n; t++) {
+        const int scaled = sm.scaled[b] < n ? sm.scaled[b] : n;
+        auto token = [&](int t, auto scaled_form) {
+            constexpr bool kScaled = decltype(scaled_form)::value;
             const float2 ad = sm.ad[b][t];
             const float4 xv = *reinterpret_cast<const float4*>(&sm.x[b][t][pg]);
             const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&sm.k[b][t][r4]);
@@ -104,11 +129,11 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
             const f2 a = pair(ad.x, ad.x);
             const f2 v[4] = {pair(xv.x * ad.y, xv.x * ad.y), pair(xv.y * ad.y, xv.y * ad.y),
                              pair(xv.z * ad.y, xv.z * ad.y), pair(xv.w * ad.y, xv.w * ad.y)};
-            if (!OUT) total *= ad.x;
+            if (!OUT && !kScaled) total *= ad.x;
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) S[i][j] = fma2(k[i], v[j], mul2(S[i][j], a));
+                for (int j = 0; j < 4; j++) S[i][j] = fma2(k[i], v[j], kScaled ? S[i][j] : mul2(S[i][j], a));
             if constexpr (OUT) {
                 const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(&sm.q[b][t][r4]);
                 const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(&sm.q[b][t][N / 2 + r4]);
@@ -124,7 +149,19 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
                 }
                 *reinterpret_cast<float4*>(&sm.part[t][tid % kL][pg]) = make_float4(o[0], o[1], o[2], o[3]);
             }
+        };
+#pragma unroll 4
+        for (int t = 0; t < scaled; t++) token(t, std::true_type{});
+        if (scaled) {
+            const float c = sm.ad[b][scaled - 1].x;
+            if (!OUT) total *= c;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) S[i][j] = mul2(S[i][j], pair(c, c));
         }
+#pragma unroll 2
+        for (int t = scaled; t < n; t++) token(t, std::false_type{});
         stage(b ^ 1);
         __syncthreads();
         if constexpr (OUT) {
@@ -134,7 +171,7 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
                 const int t = (e * kThreads + tid) / 16, c = tid % 16 * 4;
                 if (t >= n) continue;
                 const float4 x4 = *reinterpret_cast<const float4*>(&sm.x[b][t][c]);
-                float4 u = make_float4(D * x4.x, D * x4.y, D * x4.z, D * x4.w);
+                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int l = 0; l < kL; l++) {
                     const float4 v = *reinterpret_cast<const float4*>(&sm.part[t][l][c]);
@@ -143,6 +180,11 @@ __global__ void __launch_bounds__(N * 2) rec_kernel(const ScanParams p) {
                     u.z += v.z;
                     u.w += v.w;
                 }
+                const float c1 = t < scaled ? sm.ad[b][t].x : 1.0f;
+                u.x = fmaf(D, x4.x, u.x * c1);
+                u.y = fmaf(D, x4.y, u.y * c1);
+                u.z = fmaf(D, x4.z, u.z * c1);
+                u.w = fmaf(D, x4.w, u.w * c1);
                 float* const y = static_cast<float*>(p.y) + (t0 + t) * p.ys + (int64_t)h * p.dv + c0 + c;
                 if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
                     *reinterpret_cast<float4*>(y) = u;
