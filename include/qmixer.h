@@ -20,7 +20,7 @@
  *   norm       h = x + residual, x silu(gate) or x;
  *              y = h / sqrt(mean(h^2) + eps) * weight
  * The prompt scan of bfloat16 inputs forms its matrix products on the tensor
- * cores with binary32 sums; csrc/mixer/qmixer_scan_chunk.cuh says which
+ * cores with binary32 sums; csrc/mixer/qmixer_scan_chunk.cu says which
  * factors it rounds to bfloat16 there.
  *
  * SEQUENCES.  The token axis of the prompt calls holds `sequences` sequences
