@@ -47,7 +47,7 @@ constexpr int kChunk = 128;        // the chunked form's whole chunks
 struct Segment {
     int sequence;
     int64_t from, to;           // tokens
-    bool first, last;
+    bool last;                  // of its sequence
 };
 
 __device__ __forceinline__ int64_t segments_of(const ScanParams& p, int s) {
@@ -95,7 +95,6 @@ __device__ __forceinline__ bool find_segment(const ScanParams& p, int64_t g, Seg
     o.sequence = s;
     o.from = from + k * p.seg_len;
     o.to = p.cut && o.from + p.seg_len < end ? o.from + p.seg_len : end;
-    o.first = k == 0;
     o.last = o.to == end || end <= from;
     return true;
 }

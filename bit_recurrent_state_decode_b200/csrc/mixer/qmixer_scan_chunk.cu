@@ -619,6 +619,9 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
             }
             put_state();
             if (!OUT) {
+                // (not before the next decays: M, which no product waits for here, may
+                // then not fall two phases of B_E behind)
+                if (c + 1 < chunks && !wait3(B_SC, c + 1)) break;
                 warp_arrive(bars + B_E + (c & 1), lane);
                 continue;
             }
