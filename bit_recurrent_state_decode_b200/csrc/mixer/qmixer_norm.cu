@@ -9,9 +9,9 @@
 // time, all loads of a row in flight together.  The groups of the 8-bit scales are
 // powers of two of at most 256 columns: 32 lanes or fewer of one warp, joined by
 // shuffles.  Measured on 16384 rows of 2048 bfloat16: residual, output in type 42 us
-// (6.3 TB/s, 97% of the copy rate); gate to e4m3 in groups of 128 40 us (4.2 TB/s) and
-// int8 of whole rows 27 us (3.7 TB/s), both bound by instruction issue (77% of the
-// slots): what a code costs beside its bytes.
+// (6.3 TB/s, 97% of the copy rate); gate to e4m3 in groups of 128 43 us (3.9 TB/s) and
+// int8 of whole rows 27.5 us (3.7 TB/s): what a code costs beside its bytes, 2.5 and
+// 0.3 us of it for the quotients' correct rounding.
 #include "qmixer_common.cuh"
 
 namespace qm {
@@ -103,44 +103,61 @@ __device__ __forceinline__ uint32_t largest(const f2 (&h)[4]) {
 }
 
 // The scale of a group from its largest magnitude (as bits: an integer maximum
-// keeps a NaN) and the codes of eight of its values.
+// keeps a NaN) and the codes of eight of its values.  scale = most / Qmax and the
+// quotient y / scale are the correctly rounded ones: a product with the rounded
+// reciprocal, then one correction by the exact remainder (Markstein's scheme).
 struct Codes {
     float scale, inv;
-    bool odd;            // not a number, zero, or so small that its reciprocal may overflow
-    // `unit`: 1 / Qmax.  (A scale one unit off its quotient stands for the same values.)
-    __device__ __forceinline__ Codes(uint32_t most, float unit) {
-        const bool bad = most >= 0x7f800000u;
-        scale = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(most) * unit;
-        odd = !(scale >= 1e-36f);
-        inv = rcp_approx(scale);
+    bool odd;            // not a number, zero, or so small that a remainder may not be exact
+    // `unit`: RN(1 / qmax)
+    __device__ __forceinline__ Codes(uint32_t most, float qmax, float unit) {
+        const float m = __uint_as_float(most), q = m * unit;
+        scale = most >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaf(fmaf(-q, qmax, m), unit, q);
+        odd = !(scale >= 0x1p-80f);
+        if (odd && most < 0x7f800000u) scale = __fdiv_rn(m, qmax);
+        const float near = rcp_approx(scale);
+        inv = fmaf(fmaf(-scale, near, 1.0f), near, near);        // one step of Newton's
     }
-    __device__ __forceinline__ void divide(const f2 (&y)[4], float (&z)[8]) const {
-        f2 q[4];
+    __device__ __forceinline__ void divide(const f2 (&y)[4], f2 (&z)[4]) const {
+        const f2 by = pair(inv, inv), less = pair(-scale, -scale);
 #pragma unroll
-        for (int i = 0; i < 4; i++) q[i] = mul2(y[i], pair(inv, inv));
-        floats(q, z);
+        for (int i = 0; i < 4; i++) {
+            const f2 q = mul2(y[i], by);
+            z[i] = fma2(fma2(q, less, y[i]), by, q);
+        }
         if (odd) {
+            // (a scale below the normal numbers is far off its quotient: clamped)
             float v[8];
             floats(y, v);
 #pragma unroll
-            for (int i = 0; i < 8; i++) z[i] = scale > 0.0f ? __fdiv_rn(v[i], scale) : 0.0f;
+            for (int i = 0; i < 8; i++) v[i] = scale > 0.0f ? fminf(fmaxf(__fdiv_rn(v[i], scale), -448.0f), 448.0f) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) z[i] = pair(v[2 * i], v[2 * i + 1]);
         }
     }
     __device__ __forceinline__ uint2 int8(const f2 (&y)[4]) const {
-        float z[8];
+        f2 z[4];
+        float f[8];
         uint32_t c[8];
         divide(y, z);
+        // 1.5 * 2^23: rounds half to even.  (No quotient rounds beyond 127 but an odd
+        // one's, which is clamped.)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float q = fminf(fmaxf(z[i], -127.0f), 127.0f);
-            c[i] = __float_as_uint(q + 12582912.0f);              // 1.5 * 2^23: rounds half to even
-        }
+        for (int i = 0; i < 4; i++) z[i] = add2(z[i], pair(12582912.0f, 12582912.0f));
+        floats(z, f);
+        if (odd)
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] = fminf(fmaxf(f[i], 12582785.0f), 12583039.0f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] = __float_as_uint(f[i]);
         return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x40), __byte_perm(c[2], c[3], 0x40), 0x5410),
                           __byte_perm(__byte_perm(c[4], c[5], 0x40), __byte_perm(c[6], c[7], 0x40), 0x5410));
     }
     __device__ __forceinline__ uint2 e4m3(const f2 (&y)[4]) const {
+        f2 q[4];
         float z[8];
-        divide(y, z);
+        divide(y, q);
+        floats(q, z);
         return make_uint2(e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16, e4m3x2(z[4], z[5]) | e4m3x2(z[6], z[7]) << 16);
     }
 };
@@ -225,6 +242,7 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS == 128 
         return;
     }
     uint8_t* const y = static_cast<uint8_t*>(p.y) + row * p.ys;
+    const float qmax = p.out == QMIXER_OUT_INT8 ? 127.0f : 448.0f;
     const float unit = p.out == QMIXER_OUT_INT8 ? 1.0f / 127.0f : 1.0f / 448.0f;
     if (!p.group) {
         most = __reduce_max_sync(~0u, most);
@@ -245,7 +263,7 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS == 128 
             for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
         }
         if (left <= 0) continue;
-        const Codes q(m, unit);
+        const Codes q(m, qmax, unit);
         if (p.group ? (c & (p.group - 1)) == 0 : c == 0)
             p.scales[row * ngroups + (p.group ? c / p.group : 0)] = q.scale;
         const uint2 b = p.out == QMIXER_OUT_INT8 ? q.int8(h[i]) : q.e4m3(h[i]);

@@ -203,10 +203,12 @@ int qmixer_step_output(const qmixer_step_output_args* args, qstate_stream stream
  * unrounded sum; QMIXER_BEFORE_GATE normalises x silu(other).  out: the
  * inputs' type, or 8-bit codes with binary32 scales of each row (group 0) or
  * of each `group` consecutive columns (a power of two from 8 to 256 dividing
- * columns).  scale = max|y| / Qmax, Qmax 127 (int8, rounded half to even) or
- * 448 (e4m3, rounded to nearest even); where max|y| is 0 the scale and codes
- * are 0, where it is not a finite number the scale is NaN and the codes 0.
- * columns 1 to 32768. */
+ * columns).  scale = max|y| / Qmax, Qmax 127 (int8) or 448 (e4m3), code = y /
+ * scale, both quotients rounded to binary32 first, the code then half to even
+ * (int8) or to nearest even (e4m3), and clamped to Qmax.  y's own binary32
+ * value is within a few units: its root and silu are the hardware's to 2
+ * units.  Where max|y| is 0 the scale and codes are 0, where it is not a
+ * finite number the scale is NaN and the codes 0.  columns 1 to 32768. */
 typedef struct qmixer_norm_args {
     const void* x;
     int64_t x_stride;
