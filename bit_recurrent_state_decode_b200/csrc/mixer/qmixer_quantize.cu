@@ -114,7 +114,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     for (int i = 0; i < kEach; i++) {
         const int u = i * 256 + u0, r = u / kRow, c8 = u % kRow;
         float scale = __fdiv_rn(__uint_as_float(m[i]), qmax);
-        if (!p.scale_f32) scale = fminf(__half2float(__float2half_rn(scale)), 65504.0f);
+        if (!p.scale_f32) {
+            // an infinite half saturates, as in a step; one that is not a number stays so,
+            // and with it every value of its group
+            const __half hs = __float2half_rn(scale);
+            scale = __hisinf(hs) ? 65504.0f : __half2float(hs);
+        }
         const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale);
         const bool first = p.group ? c8 % lanes == 0 : u == 0;
         if (first) {

@@ -232,8 +232,10 @@ int qmixer_norm(const qmixer_norm_args* args, qstate_stream stream);
  * array [heads] of 2/4/6/8 that overrides bits (at most 512 heads).  bits 32
  * copies.  rotation 1: the rotated state S H is quantised; `ref` (NULL, or
  * the yoked reference [rows][heads][d_k][d_v]) receives what is quantised.  A
- * group whose maximum is not a finite number gets unspecified codes; binary16
- * scales saturate at 65504 (neither is counted). */
+ * group that holds a NaN gets the scale NaN, so that all its values read back
+ * as NaN and the next step counts its tile; one that holds an infinity gets
+ * the scale infinity, in binary16 65504, at which such scales saturate, and
+ * unspecified codes (neither is counted here). */
 typedef struct qmixer_quantize_args {
     const float* S;
     void* codes;

@@ -63,3 +63,51 @@ def test_norm_codes_of_the_smallest_rows(to, most):
     z = torch.where(want > 0, (y.double() / want.double()).float().clamp(-most, most), 0.0)
     want = z.round().to(torch.int8) if to is torch.int8 else z.to(torch.float8_e4m3fn)
     assert torch.equal(codes.float(), want.float())
+
+
+# ---------------------------------------------------------------- load
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("scale_dtype", [Q.F16, Q.F32])
+@pytest.mark.parametrize("bits", [2, 4, 6, 8])
+def test_load_of_states_that_are_no_numbers(bits, scale_dtype, group):
+    """A NaN stays one, for its whole group, and the next step counts it; infinities
+    leave the scale that a step's own conversion leaves; other groups are as ever."""
+    make = lambda: Q.QState(1, 3, 64, 64, Q.MAMBA2, bits=bits, group=group, scale_dtype=scale_dtype)  # noqa: E731
+    obj, clean = make(), make()
+    S = normal(gen(bits), 3, 64, 64)
+    M.load(clean, S)
+    want, (_, scales, _) = clean.dequant(), clean.export()
+    want, scales = want.clone(), scales.float().clone()
+    S[0, 5, 40], S[1, 7, 33] = float("nan"), -float("inf")
+    S[0, 5, 41] = float("inf")                       # beside the NaN, which prevails
+    M.load(obj, S)
+    got, (_, sc, _) = obj.dequant(), obj.export()
+    if group:
+        at = [(0, 5, 1), (1, 7, 1)]
+        rows = torch.zeros(3, 64, 2, dtype=torch.bool, device=DEV)
+        sc, scales = sc.float().view(3, 64, 2), scales.view(3, 64, 2)
+    else:
+        at = [(0,), (1,)]
+        rows = torch.zeros(3, dtype=torch.bool, device=DEV)
+        sc, scales = sc.float().view(3), scales.view(3)
+    for i in at:
+        rows[i] = True
+    assert bool(torch.isnan(sc[at[0]]))
+    assert float(sc[at[1]]) == (65504.0 if scale_dtype == Q.F16 else float("inf"))
+    assert torch.equal(sc[~rows], scales[~rows])
+    nan = torch.zeros(3, 64, 64, dtype=torch.bool, device=DEV)
+    nan[(0, 5, slice(32, 64)) if group else (0,)] = True
+    odd = nan.clone()
+    odd[(1, 7, slice(32, 64)) if group else (1,)] = True
+    assert bool(torch.isnan(got[nan]).all())
+    assert torch.equal(got[~odd], want[~odd])
+    # the step behind it sees both tiles (an infinite scale times a code, or a NaN)
+    q, k, v, gates, out = obj.alloc_inputs()
+    q.fill_(1.0)
+    for t in (k, v, gates):
+        t.fill_(0.5)
+    obj.step(q, k, v, gates, out)
+    assert bool(torch.isnan(out[0]).any()) and bool(torch.isfinite(out[2]).all())
+    assert obj.status()["nonfinite"] >= 1
+    obj.close()
+    clean.close()
