@@ -6,7 +6,10 @@
 // wants them on the current device and stream, with an output of its own, and
 // returns None for any other, without having launched anything: qmixer.py then
 // goes its own way, which takes the rarer forms (outputs and streams of the
-// caller's, other devices) and refuses the rest with a message.
+// caller's, other devices) and refuses the rest with a message.  Refusals of the
+// C entry come before its first launch and are left to Python too; what it reports
+// behind that, or what fails once it has returned, is raised: the state or residual
+// may have moved on, so the call must not be made again.
 #include <ATen/ATen.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -93,6 +96,33 @@ bool on16(const Tensor& t) { return (reinterpret_cast<uintptr_t>(t.data_ptr()) &
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// A call that may have launched.
+struct Launched {
+    const char* entry;
+    int rc;
+};
+
+// Whether a C entry took its call; throws where it failed behind its checks.
+bool taken(const char* entry, int rc) {
+    if (rc == QSTATE_OK) return true;
+    if (rc == QSTATE_EINVAL || rc == QSTATE_EUNSUPPORTED) return false;
+    throw Launched{entry, rc};
+}
+// The outputs of a call that was taken, as Python objects (one, or a pair).
+PyObject* wrapped(const char* entry, Tensor& y, Tensor* scales = nullptr) {
+    try {
+        PyObject* first = THPVariable_Wrap(std::move(y));
+        if (!scales) return first;
+        PyObject *second = THPVariable_Wrap(std::move(*scales)), *both = nullptr;
+        if (first && second) both = PyTuple_Pack(2, first, second);
+        Py_XDECREF(first);
+        Py_XDECREF(second);
+        return both;
+    } catch (...) {
+        throw Launched{entry, QSTATE_ENOMEM};
+    }
+}
+
 // Sequences of a prompt with `lead` leading dimensions.
 struct Prompt {
     int64_t sequences = 0, tokens = 0;
@@ -143,6 +173,7 @@ PyObject* conv_any(PyObject* const* a, bool step) {
         return none();
     Tensor y = at::empty(x->sizes(), x->options());
     const int32_t act = a[4] == Py_True ? QMIXER_SILU : 0;
+    const char* const entry = step ? "qmixer_conv_step" : "qmixer_conv";
     int rc;
     if (step) {
         const qmixer_conv_step_args q{x->data_ptr(), xs, w->data_ptr(), bias, state->data_ptr(), y.data_ptr(), channels,
@@ -154,7 +185,7 @@ PyObject* conv_any(PyObject* const* a, bool step) {
                                  (int32_t)width, type, act | (initial ? QMIXER_INITIAL : 0)};
         rc = qmixer_conv(&q, c.stream());
     }
-    return rc == QSTATE_OK ? THPVariable_Wrap(std::move(y)) : none();
+    return taken(entry, rc) ? wrapped(entry, y) : none();
 }
 
 // ---------------------------------------------------------------- selective scan
@@ -195,7 +226,8 @@ PyObject* scan_any(PyObject* const* a, bool step) {
         const qmixer_scan_step_args q{x->data_ptr(), xs, dt->data_ptr(), dts, A, B->data_ptr(), Bs, C->data_ptr(), Cs, D,
                                       bias, S, y.data_ptr(), heads * d_v, (int32_t)x->size(0), (int32_t)heads,
                                       (int32_t)groups, (int32_t)d_k, (int32_t)d_v, type, dt_type, flags};
-        return qmixer_scan_step(&q, c.stream()) == QSTATE_OK ? THPVariable_Wrap(std::move(y)) : none();
+        const char* const entry = "qmixer_scan_step";
+        return taken(entry, qmixer_scan_step(&q, c.stream())) ? wrapped(entry, y) : none();
     }
     const int64_t bytes = qmixer_scan_workspace((int32_t)p.sequences, p.tokens, (int32_t)heads, (int32_t)groups,
                                                 (int32_t)d_k, (int32_t)d_v, type);
@@ -206,7 +238,8 @@ PyObject* scan_any(PyObject* const* a, bool step) {
                              y.data_ptr(), heads * d_v, p.starts, (int32_t)p.sequences, p.tokens, (int32_t)heads,
                              (int32_t)groups, (int32_t)d_k, (int32_t)d_v, type, dt_type, flags,
                              bytes ? work.data_ptr() : nullptr, bytes};
-    return qmixer_scan(&q, c.stream()) == QSTATE_OK ? THPVariable_Wrap(std::move(y)) : none();
+    const char* const entry = "qmixer_scan";
+    return taken(entry, qmixer_scan(&q, c.stream())) ? wrapped(entry, y) : none();
 }
 
 // ---------------------------------------------------------------- norm
@@ -248,21 +281,28 @@ PyObject* norm_any(PyObject* const* a) {
     const qmixer_norm_args q{x->data_ptr(), xs, other ? other->data_ptr() : nullptr, os, w, y.data_ptr(), columns,
                              kind ? static_cast<float*>(scales.data_ptr()) : nullptr, x->numel() / columns,
                              (int32_t)columns, (int32_t)group, (float)eps, type, (int32_t)before, (int32_t)kind};
-    if (qmixer_norm(&q, c.stream()) != QSTATE_OK) return none();
-    if (!kind) return THPVariable_Wrap(std::move(y));
-    PyObject *py = THPVariable_Wrap(std::move(y)), *ps = THPVariable_Wrap(std::move(scales));
-    PyObject* both = py && ps ? PyTuple_Pack(2, py, ps) : nullptr;
-    Py_XDECREF(py);
-    Py_XDECREF(ps);
-    return both;
+    const char* const entry = "qmixer_norm";
+    if (!taken(entry, qmixer_norm(&q, c.stream()))) return none();
+    return wrapped(entry, y, kind ? &scales : nullptr);
 }
 
 // ---------------------------------------------------------------- module
-// No exception leaves: a failed allocation, say, is left to the Python way, which
-// meets it again and raises it.
+// No C++ exception leaves.  One in front of the launch, of a failed allocation, say,
+// is left to the Python way, which meets it again and raises it.
 template <class F> PyObject* guarded(F f) {
     try {
         return f();
+    } catch (const Launched& e) {
+        // QStateError(entry, code), as from Python
+        PyErr_Clear();
+        PyObject* const home = PyImport_ImportModule("bit_recurrent_state_decode_b200.qstate");
+        PyObject* const type = home ? PyObject_GetAttrString(home, "QStateError") : nullptr;
+        PyObject* const args = type ? Py_BuildValue("(si)", e.entry, e.rc) : nullptr;
+        if (args) PyErr_SetObject(type, args);
+        Py_XDECREF(args);
+        Py_XDECREF(type);
+        Py_XDECREF(home);
+        return nullptr;
     } catch (...) {
         return none();
     }

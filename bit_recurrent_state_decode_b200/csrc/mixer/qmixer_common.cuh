@@ -150,13 +150,15 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 inline bool known(int32_t dtype) { return dtype == QSTATE_F32 || dtype == QSTATE_BF16; }
 inline int size_of(int32_t dtype) { return dtype == QSTATE_BF16 ? 2 : 4; }
 // Let a kernel take more dynamic shared memory than 48 KB, once per device.
-// `done` is the kernel's own mask of devices.
+// `done` is the kernel's own mask of devices.  (A failure leaves no error behind
+// that the next call's launched() would take for its own.)
 inline bool allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError(), false;
     const uint64_t bit = 1ull << (dev & 63);
     if (done.load(std::memory_order_relaxed) & bit) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return cudaGetLastError(), false;
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
 }

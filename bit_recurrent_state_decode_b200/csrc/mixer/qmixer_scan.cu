@@ -161,9 +161,8 @@ int qmixer_scan(const qmixer_scan_args* args, qstate_stream stream) {
     // (without tokens only states are set: any form does)
     const bool chunked = a.dtype == QSTATE_BF16 && a.tokens > 0;
     auto launch = [&](bool states_only) {
-        if (chunked) return qm::launch_scan_chunk(p, a.d_k, plan.segments, states_only, st);
-        qm::launch_scan_rec(p, a.d_k, plan.segments, states_only, st);
-        return true;
+        return chunked ? qm::launch_scan_chunk(p, a.d_k, plan.segments, states_only, st)
+                       : qm::launch_scan_rec(p, a.d_k, plan.segments, states_only, st);
     };
     if (plan.cut) {
         if (!launch(true)) return QSTATE_ECUDA;

@@ -100,8 +100,9 @@ __device__ __forceinline__ bool find_segment(const ScanParams& p, int64_t g, Seg
 }
 
 // The kernels of the recurrent form (binary32) and of the chunked form (bfloat16,
-// tensor cores): states only (launch 1) or the whole scan.
-void launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
+// tensor cores): states only (launch 1) or the whole scan.  False, with nothing
+// launched and no error left behind, where a launch cannot be prepared.
+bool launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
 bool launch_scan_chunk(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
 
 }  // namespace qm

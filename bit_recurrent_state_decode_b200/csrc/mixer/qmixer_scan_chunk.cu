@@ -717,8 +717,10 @@ EncodeFn encoder() {
         void* at = nullptr;
         cudaDriverEntryPointQueryResult found;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();          // none is left for the next call
             return nullptr;
+        }
         f = reinterpret_cast<EncodeFn>(at);
         fn.store(f, std::memory_order_release);
     }

@@ -214,22 +214,21 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
 }
 
 template <int N, bool OUT>
-void launch_rec(const ScanParams& p, int64_t segments, cudaStream_t st) {
+bool launch_rec(const ScanParams& p, int64_t segments, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(reinterpret_cast<const void*>(rec_kernel<N, OUT>), sizeof(RecSmem<N, OUT>), done)) return;
+    if (!allow_smem(reinterpret_cast<const void*>(rec_kernel<N, OUT>), sizeof(RecSmem<N, OUT>), done)) return false;
     const dim3 grid((unsigned)segments, (unsigned)(p.heads * (p.dv / 64)));
     rec_kernel<N, OUT><<<grid, N * 2, sizeof(RecSmem<N, OUT>), st>>>(p);
+    return true;
 }
 
 template <int N>
-void launch_rec(const ScanParams& p, int64_t segments, bool states_only, cudaStream_t st) {
-    if (states_only) launch_rec<N, false>(p, segments, st);
-    else launch_rec<N, true>(p, segments, st);
+bool launch_rec(const ScanParams& p, int64_t segments, bool states_only, cudaStream_t st) {
+    return states_only ? launch_rec<N, false>(p, segments, st) : launch_rec<N, true>(p, segments, st);
 }
 
-void launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st) {
-    if (dk == 64) launch_rec<64>(p, segments, states_only, st);
-    else launch_rec<128>(p, segments, states_only, st);
+bool launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st) {
+    return dk == 64 ? launch_rec<64>(p, segments, states_only, st) : launch_rec<128>(p, segments, states_only, st);
 }
 
 }  // namespace qm

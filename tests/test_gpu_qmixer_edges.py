@@ -111,3 +111,47 @@ def test_load_of_states_that_are_no_numbers(bits, scale_dtype, group):
     assert obj.status()["nonfinite"] >= 1
     obj.close()
     clean.close()
+
+
+# ---------------------------------------------------------------- errors behind a launch
+CHILD = """
+import ctypes, os, sys, torch
+from bit_recurrent_state_decode_b200 import qmixer as M, qstate as Q
+count = ctypes.c_int.in_dll(ctypes.CDLL(os.environ["LD_PRELOAD"]), "calls")
+x = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+dt, A = torch.ones(4, 2, device="cuda"), -torch.ones(2, device="cuda")
+one, st = torch.ones(1, 2, 64, 64, device="cuda"), torch.ones(4, 2, 64, 64, device="cuda")
+c, w = x[:, 0].contiguous(), torch.ones(64, 4, dtype=torch.bfloat16, device="cuda")
+c1, cs = torch.ones(1, 3, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(4, 3, 64, dtype=torch.bfloat16, device="cuda")
+res = torch.ones_like(c)
+calls = [(lambda: M.conv(c, w, state=c1, initial=True), c1), (lambda: M.conv_step(c, w, state=cs), cs),
+         (lambda: M.scan(x, dt, A, x, x, state=one, initial=True), one), (lambda: M.scan_step(x, dt, A, x, x, state=st), st),
+         (lambda: M.norm(c, w[:, 0].contiguous(), residual=res), res)]
+for i, (call, kept) in enumerate(calls):
+    before = kept.clone()
+    try:
+        call()
+        sys.exit(f"call {i} was made again")
+    except Q.QStateError as e:
+        assert e.code == Q.ECUDA, e
+    torch.cuda.synchronize()
+    assert count.value == i + 1 and torch.equal(kept, before), (i, count.value)
+print("once each")
+"""
+
+
+def test_an_error_behind_the_launch_is_raised_and_the_call_not_repeated(tmp_path):
+    """C entries that report a CUDA error: the compiled calls raise it after one call.
+    (A second one, by way of Python, would move states and residuals on again.)"""
+    import os
+    import subprocess
+    import sys
+    names = ("conv", "conv_step", "scan", "scan_step", "norm")
+    src, so = tmp_path / "stand_in.c", str(tmp_path / "stand_in.so")
+    src.write_text("int calls;\n" + "".join(f"int qmixer_{n}(const void* a, void* s) {{ (void)a; (void)s; calls++; return -3; }}\n"
+                                             for n in names))
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", so], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, cwd=root, timeout=300,
+                       env={**os.environ, "LD_PRELOAD": so, "PYTHONPATH": root})
+    assert r.returncode == 0 and r.stdout.strip() == "once each", r.stdout + r.stderr
