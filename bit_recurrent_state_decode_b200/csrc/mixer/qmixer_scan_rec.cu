@@ -9,13 +9,20 @@
 // the state is kept divided by c_t, the product of the batch's decays up to t:
 //   S_t / c_t = S_{t-1} / c_{t-1} + (dt x / c_t) B^T,  y = c_t (S_t / c_t)^T C + D x
 // which spares the decay's multiplication of every element (a third of the
-// instructions), as long as every c_t lies in 2^-40 .. 2^40; from the first token on
-// that leaves it, the batch takes the plain form.  A token then costs 32 packed instructions and five
+// instructions).  It must not cost range: what is divided by c may not overflow where
+// the plain form would not.  So it holds while c_t >= 2^-40, decays are at most 1 and
+// finite inputs are moderate: |x|, |B|, |C| < 2^13, |dt| < 2^7, the state in front of the
+// segment below 2^64.  A token then adds less than 2^33 to an element, the fewer than
+// 2^31 tokens of a sequence less than 2^64, and the largest value that is formed, a sum
+// of y over 128 rows, stays below 2^13 2^65 2^7 2^40 = 2^125.  From the first token on
+// whose c leaves its range the batch takes the plain form, from the first that breaks
+// another of these bounds on all of the segment: whatever a later token holds, an
+// earlier one is computed alike.  A token then costs 32 packed instructions and five
 // 16-byte shared loads a thread: instruction issue is the bound, not memory.  kBatch tokens are staged at a time while the next ones are on
 // their way to registers.  The 8 or 16 threads of a column leave their parts of y in
 // shared memory, where they are added once per batch (shuffles within the token
 // took a fifth of the instructions and most of the waiting).  Eight sequences of 1024
-// tokens, 32 heads of 128 x 64, take 333 us (367 with the decay in every token); the
+// tokens, 32 heads of 128 x 64, take 344 us (367 with the decay in every token); the
 // packed instructions alone would take 120, issuing every other cycle.
 #include <type_traits>
 
@@ -24,7 +31,20 @@
 namespace qm {
 
 constexpr int kBatch = kBatchTokens;
-constexpr float kLeast = 0x1p-40f;
+constexpr float kLeast = 0x1p-40f, kMostInput = 0x1p13f, kMostStep = 0x1p7f, kMostState = 0x1p64f;
+
+// Whether a finite one of eight values reaches `limit`.  (Infinities and NaN are the
+// same in either form, and leave the rest of their token as it is.)
+__device__ __forceinline__ bool large(const float (&v)[8], float limit) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+    if (m < limit) return false;
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 8; j++) any |= fabsf(v[j]) >= limit && fabsf(v[j]) < INFINITY;
+    return any;
+}
 
 template <int N, bool OUT> struct RecSmem {
     static constexpr int kOut = OUT ? kBatch : 1;
@@ -33,8 +53,10 @@ template <int N, bool OUT> struct RecSmem {
     alignas(16) float x[2][kBatch][64];
     alignas(16) float q[2][kOut][N];
     alignas(16) float part[kOut][N / 8][68];     // a row of 64 shifted by four banks against the next
-    alignas(16) float2 ad[2][kBatch];            // decay and time step, or their scaled forms
-    int scaled[2];               // so many leading tokens in the scaled form
+    alignas(16) float2 ad[2][kBatch];            // decay and time step
+    alignas(16) float2 cd[2][kBatch];            // product of the batch's decays, time step / it
+    int scaled[2];               // so many leading tokens in the scaled form, as far as c goes
+    int plain;                   // the segment's first token from which on no form but the plain one will do
 };
 
 template <int N, bool OUT>
@@ -50,6 +72,8 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
     const int g = h / p.per_group, r4 = tid % kL * 4, pg = tid / kL * 4;
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, D = OUT && p.D ? p.D[h] : 0.0f;
 
+    if (tid == 0) sm.plain = INT32_MAX;
+    __syncthreads();
     // rows r4 .. r4+3 and N/2 + r4 .. : four pairs of rows, four columns
     f2 S[4][4];
     const float* from = nullptr;
@@ -67,6 +91,8 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
         S[i][1] = pair(lo.y, hi.y);
         S[i][2] = pair(lo.z, hi.z);
         S[i][3] = pair(lo.w, hi.w);
+        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (large(v, kMostState)) atomicMin(&sm.plain, 0);
     }
 
     // staging: thread t brings eight elements of k and q (row t / (N/8)) and,
@@ -89,7 +115,10 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
             na = expf(nd * A);
         }
     };
-    auto stage = [&](int b) {
+    // the batch that starts at token t0 of the segment
+    auto stage = [&](int b, int t0) {
+        if (large(nk, kMostInput) || (OUT && large(nq, kMostInput))) atomicMin(&sm.plain, t0 + kr);
+        if (large(nx, kMostInput)) atomicMin(&sm.plain, t0 + xr);
         store8(&sm.k[b][kr][kc], nk);
         if (OUT) store8(&sm.q[b][kr][kc], nq);
         if (tid < 128) store8(&sm.x[b][xr][xc], nx);
@@ -101,11 +130,12 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
                 const float u = __shfl_up_sync(~0u, c, d);
                 if (tid >= d) c *= u;
             }
-            const bool fits = c >= kLeast && c <= 1.0f / kLeast;
-            // the tokens in front of the first that leaves the range: whatever a later
-            // token holds, an earlier one is computed alike
-            const int first = __ffs(__ballot_sync(~0u, !fits || tid >= kBatch)) - 1;
-            if (tid < kBatch) sm.ad[b][tid] = tid < first ? make_float2(c, __fdiv_rn(nd, c)) : make_float2(na, nd);
+            const int first = __ffs(__ballot_sync(~0u, !(c >= kLeast) || tid >= kBatch)) - 1;
+            if (!(na <= 1.0f && fabsf(nd) < kMostStep)) atomicMin(&sm.plain, t0 + tid);
+            if (tid < kBatch) {
+                sm.ad[b][tid] = make_float2(na, nd);
+                sm.cd[b][tid] = make_float2(c, __fdiv_rn(nd, c));
+            }
             if (tid == 0) sm.scaled[b] = first;
         }
     };
@@ -113,15 +143,19 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
     float total = 1.0f;
     int b = 0;
     fetch(seg.from);
-    stage(0);
+    stage(0, 0);
     __syncthreads();
     for (int64_t t0 = seg.from; t0 < seg.to; t0 += kBatch, b ^= 1) {
         fetch(t0 + kBatch);
         const int n = seg.to - t0 < kBatch ? (int)(seg.to - t0) : kBatch;
-        const int scaled = sm.scaled[b] < n ? sm.scaled[b] : n;
+        const int at = (int)(t0 - seg.from);
+        int scaled = sm.scaled[b] < n ? sm.scaled[b] : n;
+        // (what a thread already ahead finds in the next batch changes nothing here)
+        const int plain = *const_cast<volatile int*>(&sm.plain) - at;
+        if (plain < scaled) scaled = plain > 0 ? plain : 0;
         auto token = [&](int t, auto scaled_form) {
             constexpr bool kScaled = decltype(scaled_form)::value;
-            const float2 ad = sm.ad[b][t];
+            const float2 ad = kScaled ? sm.cd[b][t] : sm.ad[b][t];
             const float4 xv = *reinterpret_cast<const float4*>(&sm.x[b][t][pg]);
             const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&sm.k[b][t][r4]);
             const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&sm.k[b][t][N / 2 + r4]);
@@ -153,7 +187,7 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
 #pragma unroll 4
         for (int t = 0; t < scaled; t++) token(t, std::true_type{});
         if (scaled) {
-            const float c = sm.ad[b][scaled - 1].x;
+            const float c = sm.cd[b][scaled - 1].x;
             if (!OUT) total *= c;
 #pragma unroll
             for (int i = 0; i < 4; i++)
@@ -162,7 +196,7 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
         }
 #pragma unroll 2
         for (int t = scaled; t < n; t++) token(t, std::false_type{});
-        stage(b ^ 1);
+        stage(b ^ 1, at + kBatch);
         __syncthreads();
         if constexpr (OUT) {
             // token and four columns a thread, in 256 / kThreads rounds
@@ -180,7 +214,7 @@ __global__ void __launch_bounds__(N * 2, N == 128 ? 2 : 3) rec_kernel(const Scan
                     u.z += v.z;
                     u.w += v.w;
                 }
-                const float c1 = t < scaled ? sm.ad[b][t].x : 1.0f;
+                const float c1 = t < scaled ? sm.cd[b][t].x : 1.0f;
                 u.x = fmaf(D, x4.x, u.x * c1);
                 u.y = fmaf(D, x4.y, u.y * c1);
                 u.z = fmaf(D, x4.z, u.z * c1);

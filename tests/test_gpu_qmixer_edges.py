@@ -6,6 +6,8 @@ import torch
 from bit_recurrent_state_decode_b200 import qmixer as M
 from bit_recurrent_state_decode_b200 import qstate as Q
 
+from qmixer_util import half, scan_exact, within
+
 pytestmark = pytest.mark.gpu
 BF, F = torch.bfloat16, torch.float32
 DEV = "cuda"
@@ -155,3 +157,46 @@ def test_an_error_behind_the_launch_is_raised_and_the_call_not_repeated(tmp_path
     r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, cwd=root, timeout=300,
                        env={**os.environ, "LD_PRELOAD": so, "PYTHONPATH": root})
     assert r.returncode == 0 and r.stdout.strip() == "once each", r.stdout + r.stderr
+
+
+# ---------------------------------------------------------------- range of the float32 scan
+LARGE = {
+    # what is large, and the time step: decays of e^-1.7 leave 2^-40 within 17 tokens
+    "x": dict(x=1e30), "x once": dict(x_at=1e30), "B": dict(B=1e31), "C": dict(C=1e33), "state": dict(state=1e33),
+    "step": dict(dt=1e20, A=-1.7e-20), "slow": dict(x=1e30, A=-1e-3), "growth": dict(A=2.5, T=30), "just below": dict(x=8191.0, B=8191.0),
+}
+
+
+@pytest.mark.parametrize("T", [16, 70, 2500])
+@pytest.mark.parametrize("N,P", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("name", sorted(LARGE))
+def test_scan_f32_keeps_its_range(name, N, P, T):
+    """Inputs, states and steps far beyond a model's under strong decays: every value
+    that binary32 holds comes out, long and short, in one piece and cut."""
+    kw = LARGE[name]
+    T = min(T, kw.get("T", T))
+    g = gen(T + N)
+    x, B, C = normal(g, T, 1, P) * kw.get("x", 1.0), normal(g, T, 1, N) * kw.get("B", 1.0), normal(g, T, 1, N) * kw.get("C", 1.0)
+    if "x_at" in kw:
+        x[T // 2] *= kw["x_at"]
+    dt = torch.full((T, 1), kw.get("dt", 1.0), device=DEV) * (torch.rand(T, 1, device=DEV, generator=g) + 0.5)
+    A = torch.full((1,), kw.get("A", -1.7), device=DEV)
+    D = torch.ones(1, device=DEV)
+    st = normal(g, 1, 1, N, P) * kw.get("state", 1.0)
+    want = scan_exact(x, dt, A, B, C, D, None, False, st, [0, T])
+    assert bool((want[4] < 1e38).all())                       # no sum of magnitudes leaves the range
+    y = M.scan(x[None], dt[None], A, B[None], C[None], D, softplus=False, state=st, initial=True)
+    within("y", y[0], want[0], want[2] + half(F) * (want[0].abs() + want[2]))
+    within("state", st, want[1], want[3])
+
+
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("what", ["x", "B", "C", "dt"])
+def test_scan_f32_large_inputs_reach_no_earlier_token(what, N):
+    g = gen(N)
+    T, at = 90, 39
+    x, B, C = normal(g, T, 2, 64), normal(g, T, 1, N), normal(g, T, 1, N)
+    dt, A = torch.rand(T, 2, device=DEV, generator=g), torch.tensor([-1.0, -4.0], device=DEV)
+    clean = M.scan(x, dt, A, B, C, softplus=False)
+    {"x": x, "B": B, "C": C, "dt": dt}[what][at].view(-1)[1] = 1e9
+    assert torch.equal(M.scan(x, dt, A, B, C, softplus=False)[:at], clean[:at])
