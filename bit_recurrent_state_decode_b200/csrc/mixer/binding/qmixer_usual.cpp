@@ -26,7 +26,8 @@ struct Call {
     bool ok = true;
     int device = -1;
 
-    // a CUDA tensor of the current device that no gradient is wanted for
+    // a CUDA tensor of the current device that no gradient is wanted for and that
+    // carries no forward-mode tangent
     const Tensor* tensor(PyObject* o) {
         if (!ok || !THPVariable_Check(o)) {
             ok = false;
@@ -39,6 +40,7 @@ struct Call {
             if (device != c10::cuda::current_device()) ok = false;
         } else if (t.get_device() != device) ok = false;
         if (ok && t.requires_grad() && c10::GradMode::is_enabled()) ok = false;
+        if (ok && t._fw_grad(0).defined()) ok = false;
         return ok ? &t : nullptr;
     }
     // nothing, or a contiguous vector of n

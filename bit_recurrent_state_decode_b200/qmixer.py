@@ -13,7 +13,8 @@ launched by the compiled module _qmixer_usual; what that leaves takes the way be
 device, or on `stream`; tensors of another stream have to be ordered before
 the call by the caller, as for any PyTorch operator.  The library must have
 been built; there is no CPU fallback and no autograd: inputs that require a
-gradient are refused while gradients are recorded.
+gradient are refused while gradients are recorded, inputs with a forward-mode
+tangent always.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ import os
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from . import qstate as Q
 from .qstate import QStateError
@@ -108,7 +110,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _tensor(fn, name, t, index, dtype=None, shape=None):
     """Refuse what is not a CUDA tensor of this device (None: any), type and shape
-    (None: any), or wants a gradient."""
+    (None: any), whose memory does not hold its values (negated views, sparse
+    layouts), or that carries or wants a gradient, in either direction."""
     if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor")
     if index is not None and t.get_device() != index:
@@ -117,8 +120,12 @@ def _tensor(fn, name, t, index, dtype=None, shape=None):
         raise ValueError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.layout is not torch.strided or t.is_neg() or t.is_conj():
+        raise ValueError(f"{fn}: {name} is a view whose memory does not hold its values (resolve_neg() gives one)")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{fn}: {name} requires a gradient, and {fn} has no backward pass")
+    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{fn}: {name} carries a tangent, and {fn} has no forward-mode derivative")
 
 
 def _dense(fn, name, t, index, dtype, shape):
@@ -334,36 +341,16 @@ def _selective(fn, x, dt, A, B, C, D, dt_bias):
     groups, d_k = bsh[-2], bsh[-1]
     if groups == 0 or heads % groups:
         raise ValueError(f"{fn}: {heads} heads do not divide into {groups} groups")
-    if not _operands_hold(index, dtype, C, bsh, dt, lead + per_head, A, D, dt_bias, per_head):
-        # one of them is refused, or unusual: each by itself
-        _tensor(fn, "dt", dt, index, None, lead + per_head)
-        _tensor(fn, "C", C, index, dtype, bsh)
-        for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-            if t is not None or name == "A":
-                _dense(fn, name, t, index, _F32, per_head)
-    rows = (x.data_ptr(), _rows2(fn, "x", x, d_v, heads * d_v), dt.data_ptr(), _rows(fn, "dt", dt, 1), A.data_ptr(),
+    _tensor(fn, "dt", dt, index, None, lead + per_head)
+    _tensor(fn, "C", C, index, dtype, bsh)
+    ap = _dense(fn, "A", A, index, _F32, per_head)
+    dp, biasp = (0 if t is None else _dense(fn, name, t, index, _F32, per_head)
+                 for name, t in (("D", D), ("dt_bias", dt_bias)))
+    rows = (x.data_ptr(), _rows2(fn, "x", x, d_v, heads * d_v), dt.data_ptr(), _rows(fn, "dt", dt, 1), ap,
             B.data_ptr(), _rows2(fn, "B", B, d_k, groups * d_k), C.data_ptr(), _rows2(fn, "C", C, d_k, groups * d_k))
     if (rows[0] | rows[5] | rows[7] | (rows[1] | rows[6] | rows[8]) * x.element_size()) & 15:
         raise ValueError(f"{fn}: the rows of x, B and C must start on 16-byte boundaries")
-    return (rows, 0 if D is None else D.data_ptr(), 0 if dt_bias is None else dt_bias.data_ptr(),
-            (heads, groups, d_k, d_v, code, _code(fn, dt)), index)
-
-
-def _operands_hold(index, dtype, C, csh, dt, dsh, A, D, dt_bias, per_head):
-    """Whether the checks of _selective hold for these, without their messages."""
-    try:
-        if not (C.get_device() == dt.get_device() == A.get_device() == index and C.dtype is dtype and A.dtype is _F32
-                and C.shape == csh and dt.shape == dsh and A.shape == per_head and A.is_contiguous()):
-            return False
-        grad = C.requires_grad or dt.requires_grad or A.requires_grad
-        for t in (D, dt_bias):
-            if t is not None:
-                if not (t.get_device() == index and t.dtype is _F32 and t.shape == per_head and t.is_contiguous()):
-                    return False
-                grad = grad or t.requires_grad
-        return not (grad and torch.is_grad_enabled())
-    except AttributeError:      # not a tensor
-        return False
+    return rows, dp, biasp, (heads, groups, d_k, d_v, code, _code(fn, dt)), index
 
 
 def _rows2(fn, name, t, inner, row):

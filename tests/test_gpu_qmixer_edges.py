@@ -200,3 +200,46 @@ def test_scan_f32_large_inputs_reach_no_earlier_token(what, N):
     clean = M.scan(x, dt, A, B, C, softplus=False)
     {"x": x, "B": B, "C": C, "dt": dt}[what][at].view(-1)[1] = 1e9
     assert torch.equal(M.scan(x, dt, A, B, C, softplus=False)[:at], clean[:at])
+
+
+# ---------------------------------------------------------------- tensors that are refused
+def operands():
+    g = gen(3)
+    x, w = normal(g, 4, 64), normal(g, 64, 4)
+    s = dict(x=normal(g, 4, 2, 64), dt=normal(g, 4, 2), A=-torch.rand(2, device=DEV, generator=g), B=normal(g, 4, 2, 64),
+             C=normal(g, 4, 2, 64), D=normal(g, 2), dt_bias=normal(g, 2))
+    return {
+        "conv": (M.conv, dict(x=x, weight=w, bias=w[:, 0].contiguous(), state=normal(g, 1, 3, 64)), dict(initial=True)),
+        "conv_step": (M.conv_step, dict(x=x, weight=w, bias=w[:, 0].contiguous(), state=normal(g, 4, 3, 64)), {}),
+        "scan": (M.scan, dict(**s, state=normal(g, 1, 2, 64, 64)), dict(initial=True)),
+        "scan_step": (M.scan_step, dict(**s, state=normal(g, 4, 2, 64, 64)), {}),
+        "norm": (M.norm, dict(x=x, weight=w[:, 0].contiguous(), residual=normal(g, 4, 64)), {}),
+        "norm gated": (M.norm, dict(x=x, weight=w[:, 0].contiguous(), gate=normal(g, 4, 64)), {}),
+        "load": (lambda S: M.load(obj_of(), S), dict(S=normal(g, 2, 64, 64)), {}),
+        "step": (lambda **kw: M.step(obj_of(4), **kw), s, {}),
+    }
+
+
+def obj_of(batch=1):
+    return Q.QState(batch, 2, 64, 64, Q.MAMBA2, bits=8, group=32)
+
+
+@pytest.mark.parametrize("name", ["conv", "conv_step", "scan", "scan_step", "norm", "norm gated", "load", "step"])
+def test_tangents_and_negated_views_are_refused(name):
+    """An input with a forward-mode tangent would lose it, one with the negative bit
+    would be read without its sign: each operand of each operator is refused by name."""
+    from torch.autograd import forward_ad
+    fn, tensors, kw = operands()[name]
+    keep = {n: t.clone() for n, t in tensors.items()}
+    for arg, t in tensors.items():
+        with forward_ad.dual_level(), pytest.raises(ValueError, match=f"{arg} carries a tangent"):
+            fn(**{**tensors, arg: forward_ad.make_dual(t, torch.ones_like(t))}, **kw)
+        # the imaginary part of a conjugate view, and the same bit on a dense tensor
+        neg = torch._neg_view(t)
+        assert neg.is_neg()
+        with pytest.raises(ValueError, match=f"{arg} is a view"):
+            fn(**{**tensors, arg: neg}, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(tensors[n], keep[n]) for n in tensors), arg
+    with forward_ad.dual_level():                             # no tangent: as ever
+        fn(**tensors, **kw)
