@@ -114,9 +114,25 @@ int check_scan(int sequences, int64_t tokens, int heads, int groups, int dk, int
     return QSTATE_OK;
 }
 
+// What qmixer_debug_set set for the scans after it.
+std::atomic<uint32_t> wait_polls{kWaitPolls};
+std::atomic<int32_t> drop_from{-1};
+
 }  // namespace qm
 
 extern "C" {
+
+int qmixer_scan_timeouts(uint64_t* count, qstate_stream stream) {
+    if (!count) return QSTATE_EINVAL;
+    return qm::scan_timeouts(count, (cudaStream_t)stream) ? QSTATE_OK : QSTATE_ECUDA;
+}
+
+int qmixer_debug_set(int32_t drop_from_chunk, uint32_t wait_polls) {
+    if (drop_from_chunk < -1 || !wait_polls) return QSTATE_EINVAL;
+    qm::drop_from.store(drop_from_chunk, std::memory_order_relaxed);
+    qm::wait_polls.store(wait_polls, std::memory_order_relaxed);
+    return QSTATE_OK;
+}
 
 int64_t qmixer_scan_workspace(int32_t sequences, int64_t tokens, int32_t heads, int32_t groups, int32_t d_k,
                               int32_t d_v, int32_t dtype) {
@@ -156,7 +172,8 @@ int qmixer_scan(const qmixer_scan_args* args, qstate_stream stream) {
                      {a.seq_starts, a.sequences, a.tokens, a.tokens / a.sequences}, a.heads, a.heads / a.groups, a.d_v,
                      a.dt_dtype == QSTATE_BF16, (a.flags & QMIXER_SOFTPLUS) != 0, (a.flags & QMIXER_INITIAL) != 0,
                      plan.seg_len, plan.segments, plan.cut, static_cast<float*>(a.workspace),
-                     plan.cut ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.state_bytes) : nullptr};
+                     plan.cut ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.state_bytes) : nullptr,
+                     qm::wait_polls.load(std::memory_order_relaxed), qm::drop_from.load(std::memory_order_relaxed)};
     const cudaStream_t st = (cudaStream_t)stream;
     // (without tokens only states are set: any form does)
     const bool chunked = a.dtype == QSTATE_BF16 && a.tokens > 0;

@@ -39,7 +39,11 @@ struct ScanParams {
     bool cut;                   // more than one segment a sequence may be there
     float* seg_state;           // [segments][heads][d_k][d_v], where cut
     float* seg_decay;           // [segments][heads]
+    uint32_t polls;             // of a wait, before it is given up
+    int32_t drop_from;          // chunks from this one on are never loaded; -1: off
 };
+
+constexpr uint32_t kWaitPolls = 1u << 24;      // several seconds
 
 constexpr int kBatchTokens = 16;   // the recurrent form's segments are whole batches,
 constexpr int kChunk = 128;        // the chunked form's whole chunks
@@ -104,5 +108,7 @@ __device__ __forceinline__ bool find_segment(const ScanParams& p, int64_t g, Seg
 // launched and no error left behind, where a launch cannot be prepared.
 bool launch_scan_rec(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
 bool launch_scan_chunk(const ScanParams& p, int dk, int64_t segments, bool states_only, cudaStream_t st);
+// CTAs of the chunked form on the current device that gave up a wait, once `st` has run.
+bool scan_timeouts(uint64_t* count, cudaStream_t st);
 
 }  // namespace qm

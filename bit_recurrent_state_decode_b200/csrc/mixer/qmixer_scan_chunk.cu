@@ -51,7 +51,11 @@
 
 namespace qm {
 
-constexpr uint32_t kPolls = 1u << 24;      // several seconds
+// Every wait is bounded: by ScanParams::polls, or, for a CTA's own copies and products,
+// which end by themselves, by kWaitPolls.  A wait that runs out (a GPU preempted for
+// seconds) ends its role; what waits for that role runs out in turn, no copy or product
+// outlives the CTA, its segment's y and state become NaN, and it is counted here.
+__device__ unsigned long long lost_ctas;
 
 // ------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -70,8 +74,8 @@ __device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
         : "memory");
     return ok;
 }
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
-    for (uint32_t i = 0; i < kPolls; i++) {
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, uint32_t polls) {
+    for (uint32_t i = 0; i < polls; i++) {
         uint32_t ok;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -233,6 +237,7 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
     int* const bad = reinterpret_cast<int*>(scal + 3);            // [2][64]: a column's first non-finite token, by chunk
     uint64_t* const bars = reinterpret_cast<uint64_t*>(bad + 128);
     uint32_t* const tm_slot = reinterpret_cast<uint32_t*>(bars + 22);
+    volatile uint32_t* const lost = tm_slot + 1;                  // set by a role that gave up
     static_assert(kBars <= 22, "room");
     constexpr uint32_t kTmem = 512;
 
@@ -248,6 +253,7 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
     const int chunks = (int)uniform((uint32_t)(seg.to > seg.from ? (seg.to - seg.from + kChunk - 1) / kChunk : 0));
 
     if (tid == 0) {
+        *lost = 0;
         for (int i = 0; i < 2; i++) {
             bar_init(bars + B_FULL + i, 2);
             bar_init(bars + B_G + i, 1);
@@ -279,10 +285,9 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
     bool ok = true;
     // wait for phase `k` of a barrier, or for chunk c's of two or three that take turns
     // (lanes of a warp may differ in when they give up: all do when one does)
-    auto wait = [&](int b, int k) { return ok = ok && __all_sync(~0u, bar_wait(bars + b, k & 1)); };
-    auto wait2 = [&](int b, int c) { return ok = ok && __all_sync(~0u, bar_wait(bars + b + (c & 1), (c >> 1) & 1)); };
-
-    auto wait3 = [&](int b, int c) { return ok = ok && __all_sync(~0u, bar_wait(bars + b + c % 3, c / 3 & 1)); };
+    auto wait = [&](int b, int k) { return ok = ok && __all_sync(~0u, bar_wait(bars + b, k & 1, p.polls)); };
+    auto wait2 = [&](int b, int c) { return ok = ok && __all_sync(~0u, bar_wait(bars + b + (c & 1), (c >> 1) & 1, p.polls)); };
+    auto wait3 = [&](int b, int c) { return ok = ok && __all_sync(~0u, bar_wait(bars + b + c % 3, c / 3 & 1, p.polls)); };
 
     if (warp == 26) {
         // ---------------------------------------------------- load
@@ -291,6 +296,7 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
             unsigned char* const st = sm + (c & 1) * L::kStage;
             uint64_t* const full = bars + B_FULL + (c & 1);
             const int t = (int)(seg.from + (int64_t)c * kChunk);
+            if (p.drop_from >= 0 && c >= p.drop_from) break;      // (for tests: these never come)
             // B and C as soon as the products have read the last ones, X when y has
             if (c >= 2 && (!wait2(B_D, c - 2) || (OUT && !wait2(B_G, c - 2)))) break;
             if (lane == 0) {
@@ -314,16 +320,20 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
             issued = c + 1;
         }
         // no copy may outlive the CTA, whatever became of its readers
-        ok = true;
-        if (half && lane == 0) bar_arrive(bars + B_FULL + (issued & 1));     // without its X
+        if (lane == 0) {
+            if (!ok) *lost = 1;          // in front of the arrival that stands for an X that never came
+            if (half) bar_arrive(bars + B_FULL + (issued & 1));
+        }
         issued += half;
-        for (int c = issued > 2 ? issued - 2 : 0; c < issued; c++) wait2(B_FULL, c);
+        for (int c = issued > 2 ? issued - 2 : 0; c < issued; c++)
+            ok = bar_wait(bars + B_FULL + (c & 1), (c >> 1) & 1, kWaitPolls) && ok;
     } else if (warp >= 24) {
         // ---------------------------------------------------- products
         // descriptors of the first stage; what follows adds multiples of 16 bytes
         const uint64_t bk = mat(smem_at(sm + L::kB), 16), ck = mat(smem_at(sm + L::kC), 16);
         const uint64_t bn = mat(smem_at(sm + L::kB), 16384), xn = mat(smem_at(sm + L::kXs), 16384);
         const uint64_t sn = mat(smem_at(sm + L::kS), 16384), wn = mat(smem_at(sm + L::kW0), 16384);
+        bool any = false;                // a product was issued
         if (warp == 24) {
             // what the states wait for: C S and the increment
             for (int c = 0; c < chunks; c++) {
@@ -331,6 +341,7 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
                 const uint32_t yo = tm + kYo + (c & 1) * 64;
                 if (!wait2(B_FULL, c) || !wait(B_S, c)) break;   // S in shared memory, the increment read
                 tc_after();
+                any = true;
                 if (OUT) {
 #pragma unroll 4
                     for (int k = 0; k < N / 16; k++)
@@ -356,6 +367,7 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
                 const uint64_t at = (uint64_t)((c & 1) * (L::kStage / 16));
                 if (!wait2(B_FULL, c)) return;
                 tc_after();
+                any = true;
 #pragma unroll 4
                 for (int k = 0; k < N / 16; k++)
                     mma_ss(tm + kG, ck + at + k / 4 * 1024 + k % 4 * 2, bk + at + k / 4 * 1024 + k % 4 * 2,
@@ -381,11 +393,11 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
                 if (next && !early) make_g(c + 1);
             }
         }
-        if (!ok) {
-            // products in flight end before tensor memory is given back
+        // products in flight end before tensor memory is given back, whoever waited for them
+        if (any) {
             __syncwarp();
             tc_commit(bars + B_DRAIN + (warp & 1));
-            (void)bar_wait(bars + B_DRAIN + (warp & 1), 0);
+            ok = bar_wait(bars + B_DRAIN + (warp & 1), 0, kWaitPolls) && ok;
         }
     } else if (warp >= 16) {
         // ---------------------------------------------------- W: half of row `r` of X
@@ -601,8 +613,7 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
         };
         put_state();
         float total = 1.0f;
-        int c = 0;
-        for (; c < chunks; c++) {
+        for (int c = 0; c < chunks; c++) {
             const Scalars& sc = scal[c % 3];
             if (!wait3(B_SC, c) || !wait2(B_D, c)) break;
             tc_after();
@@ -677,13 +688,13 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
                 for (; nans; nans &= nans - 1) reinterpret_cast<uint16_t*>(y)[__ffs((int)nans) - 1] = 0x7fc0;
             }
         }
-        if (!ok) {
-            // a wait ran out (a GPU preempted for seconds): what is left is NaN
+        if (!ok || *lost) {
+            // a wait ran out: all of the segment is NaN
             total = __uint_as_float(0x7fc00000u);
 #pragma unroll
             for (int i = 0; i < 16; i++) S[i] = pair(total, total);
             if (OUT)
-                for (int64_t t = seg.from + (int64_t)c * kChunk + row; t < seg.to; t += kChunk)
+                for (int64_t t = seg.from + row; t < seg.to; t += kChunk)
                     for (int i = 0; i < 32; i++)
                         static_cast<bf16*>(p.y)[t * p.ys + (int64_t)h * p.dv + c0 + half * 32 + i] = __float2bfloat16_rn(total);
         }
@@ -700,7 +711,9 @@ chunk_kernel(const __grid_constant__ ScanParams p, const __grid_constant__ CUten
         if (!OUT && tid == 0 && c0 == 0) p.seg_decay[(int64_t)blockIdx.x * p.heads + h] = total;
         tc_before();
     }
+    if (!ok && lane == 0) *lost = 1;
     __syncthreads();
+    if (tid == 0 && *lost) atomicAdd(&lost_ctas, 1ull);
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmem) : "memory");
 }
@@ -758,6 +771,17 @@ bool launch_scan_chunk(const ScanParams& p, int dk, int64_t segments, bool state
     if (dk == 64)
         return states_only ? launch_chunk<64, false>(p, m, segments, st) : launch_chunk<64, true>(p, m, segments, st);
     return states_only ? launch_chunk<128, false>(p, m, segments, st) : launch_chunk<128, true>(p, m, segments, st);
+}
+
+bool scan_timeouts(uint64_t* count, cudaStream_t st) {
+    unsigned long long n = 0;
+    if (cudaMemcpyFromSymbolAsync(&n, lost_ctas, sizeof(n), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    *count = n;
+    return true;
 }
 
 }  // namespace qm

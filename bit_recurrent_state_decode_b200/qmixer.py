@@ -42,7 +42,7 @@ _FIELDS = {"qmixer_conv": "PqPPPPqPiqiiii", "qmixer_conv_step": "PqPPPPqiiiii",
            "qmixer_scan": "PqPqPPqPqPPPPqPiqiiiiiiiPq", "qmixer_scan_step": "PqPqPPqPqPPPPqiiiiiiii",
            "qmixer_step_operands": "PqPqPPqPqPPPPPiiiiiiiiii", "qmixer_step_output": "PPqPPqiiii",
            "qmixer_norm": "PqPqPPqPqiifiii", "qmixer_quantize": "PPPPqiiiiPiii"}
-EXPORTS = tuple(_FIELDS) + ("qmixer_scan_workspace",)
+EXPORTS = tuple(_FIELDS) + ("qmixer_scan_workspace", "qmixer_scan_timeouts", "qmixer_debug_set")
 
 _lib = None
 
@@ -78,6 +78,8 @@ def lib():
             f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
         L.qmixer_scan_workspace.argtypes = [ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 5
         L.qmixer_scan_workspace.restype = ctypes.c_int64
+        L.qmixer_scan_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint64), ctypes.c_void_p]
+        L.qmixer_debug_set.argtypes = [ctypes.c_int32, ctypes.c_uint32]
         _lib = L
     return _lib
 
@@ -426,6 +428,26 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
               (INITIAL if initial else 0) | (SOFTPLUS if softplus else 0), work.data_ptr() if size else 0, size)
         return y
     return _launch(fn, x, stream, body)
+
+
+def scan_timeouts(device=None):
+    """Thread blocks of prompt scans on `device` (None: the current one) that gave up a
+    bounded wait so far (qmixer_scan_timeouts); their outputs and states are NaN.
+    Waits for the device's current stream."""
+    count = ctypes.c_uint64()
+    with torch.cuda.device(device):
+        rc = lib().qmixer_scan_timeouts(ctypes.byref(count), torch.cuda.current_stream().cuda_stream)
+    if rc:
+        raise QStateError("qmixer_scan_timeouts", rc)
+    return count.value
+
+
+def debug_set(drop_from_chunk=-1, wait_polls=1 << 24):
+    """Fault injection for the bounded waits of the prompt scans that follow
+    (qmixer_debug_set)."""
+    rc = lib().qmixer_debug_set(int(drop_from_chunk), int(wait_polls))
+    if rc:
+        raise QStateError("qmixer_debug_set", rc)
 
 
 def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out=None, stream=None):

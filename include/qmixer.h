@@ -55,7 +55,10 @@
  * ERRORS.  The return codes and their names are qstate.h's.  Invalid
  * arguments are rejected before any CUDA call.  Calls are asynchronous on
  * `stream`, allocate nothing, keep nothing between calls and may be captured
- * into a CUDA graph.  Buffers belong to the current device.
+ * into a CUDA graph.  Buffers belong to the current device.  The waits inside
+ * the prompt scan of bfloat16 inputs are bounded: where one runs out, y and the
+ * state of its segment and of what follows in its sequence are NaN, and
+ * qmixer_scan_timeouts counts it.
  */
 #ifndef QMIXER_H
 #define QMIXER_H
@@ -141,6 +144,18 @@ int qmixer_scan(const qmixer_scan_args* args, qstate_stream stream);
  * device; a negative return code for sizes that it refuses. */
 int64_t qmixer_scan_workspace(int32_t sequences, int64_t tokens, int32_t heads, int32_t groups,
                               int32_t d_k, int32_t d_v, int32_t dtype);
+
+/* How many thread blocks of prompt scans on the current device have given up a
+ * bounded wait since the library was loaded: 0, unless the GPU was withheld from
+ * a running kernel for seconds.  Waits for `stream`; not while it is captured. */
+int qmixer_scan_timeouts(uint64_t* count, qstate_stream stream);
+
+/* Fault injection for tests of the bounded waits, for all prompt scans of the
+ * process that follow: each wait takes at most `wait_polls` polls (default 2^24,
+ * several seconds), and the inputs of a segment's chunks of 128 tokens from
+ * drop_from_chunk on are never loaded, so that the waits for them run out; -1
+ * loads all again.  The context stays usable.  QSTATE_EINVAL for wait_polls 0. */
+int qmixer_debug_set(int32_t drop_from_chunk, uint32_t wait_polls);
 
 /* The same for one token of each sequence on binary32 states: x, y
  * [batch][heads][d_v]; every state moves on by one token. */

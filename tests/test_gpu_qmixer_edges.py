@@ -243,3 +243,59 @@ def test_tangents_and_negated_views_are_refused(name):
         assert all(torch.equal(tensors[n], keep[n]) for n in tensors), arg
     with forward_ad.dual_level():                             # no tangent: as ever
         fn(**tensors, **kw)
+
+
+# ---------------------------------------------------------------- waits that run out
+@pytest.fixture
+def short_waits():
+    """Waits of some ten milliseconds; what a test sets is taken back."""
+    yield lambda drop: M.debug_set(drop, 1 << 15)
+    M.debug_set()
+
+
+@pytest.mark.parametrize("drop", [0, 1, 2, 3])
+@pytest.mark.parametrize("N,P", [(64, 64), (128, 128)])
+def test_a_wait_that_runs_out_is_seen(N, P, drop, short_waits):
+    """Inputs that never arrive: the call ends, the whole segment is NaN, state and all,
+    the block is counted, sequences that ended before are right, and so is the next call."""
+    g = gen(drop)
+    T = [500, 100]                                           # four chunks and one
+    x, B, C = normal(g, 600, 2, P).to(BF), normal(g, 600, 1, N).to(BF), normal(g, 600, 1, N).to(BF)
+    dt, A = torch.rand(600, 2, device=DEV, generator=g), torch.tensor([-1.0, -4.0], device=DEV)
+    starts = torch.tensor([0, 500, 600], dtype=torch.int32, device=DEV)
+    call = lambda: M.scan(x, dt, A, B, C, softplus=False, seq_starts=starts, state=state)  # noqa: E731
+    state = torch.zeros(2, 2, N, P, device=DEV)
+    want, want_state = call(), state
+    before = M.scan_timeouts()
+    state = torch.zeros_like(state)
+    short_waits(drop)
+    y = call()
+    M.debug_set()
+    after = M.scan_timeouts()
+    assert bool(torch.isnan(y[:T[0]]).all()) and bool(torch.isnan(state[0]).all())
+    if drop == 0:
+        assert bool(torch.isnan(y).all()) and bool(torch.isnan(state).all())
+    else:
+        assert torch.equal(y[T[0]:], want[T[0]:]) and torch.equal(state[1], want_state[1])
+    # two heads of P / 64 blocks each
+    assert after - before == (2 if drop == 0 else 1) * 2 * (P // 64)
+    state = torch.zeros_like(state)
+    assert torch.equal(call(), want) and torch.equal(state, want_state)
+    assert M.scan_timeouts() == after
+
+
+def test_a_wait_that_runs_out_in_a_cut_scan(short_waits):
+    """The pass over the segments' states gives up too: what follows is NaN, not a
+    number that looks like one."""
+    g = gen(4)
+    x, B, C = normal(g, 4000, 1, 64).to(BF), normal(g, 4000, 1, 128).to(BF), normal(g, 4000, 1, 128).to(BF)
+    dt, A = torch.rand(4000, 1, device=DEV, generator=g) * 0.01, torch.tensor([-1.0], device=DEV)
+    assert M.lib().qmixer_scan_workspace(1, 4000, 1, 1, 128, 64, Q.BF16) > 0     # it is cut
+    want = M.scan(x, dt, A, B, C, softplus=False)
+    before = M.scan_timeouts()
+    state = torch.zeros(1, 1, 128, 64, device=DEV)
+    short_waits(1)
+    y = M.scan(x, dt, A, B, C, softplus=False, state=state)
+    M.debug_set()
+    assert bool(torch.isnan(y).all()) and bool(torch.isnan(state).all()) and M.scan_timeouts() > before
+    assert torch.equal(M.scan(x, dt, A, B, C, softplus=False), want)
