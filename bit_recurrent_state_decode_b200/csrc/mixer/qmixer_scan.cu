@@ -110,7 +110,8 @@ int check_scan(int sequences, int64_t tokens, int heads, int groups, int dk, int
     if (!known(dtype) || sequences < 0 || tokens < 0 || tokens > INT32_MAX || heads < 1 || groups < 1 ||
         heads % groups || dk < 1 || dv < 1)
         return QSTATE_EINVAL;
-    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128) || heads * (dv / 64) > 65535) return QSTATE_EUNSUPPORTED;
+    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128) || (int64_t)heads * (dv / 64) > 65535)
+        return QSTATE_EUNSUPPORTED;
     return QSTATE_OK;
 }
 
