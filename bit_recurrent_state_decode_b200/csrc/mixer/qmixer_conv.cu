@@ -288,7 +288,7 @@ int conv_any(ConvParams& p, int width, int dtype, bool step, cudaStream_t st) {
     p.vecs = vec ? p.channels / wide : p.channels;
     p.wide_taps = aligned(p.w, 16) && aligned(p.bias, 16);
     p.walks = (p.seq.tokens + kWalk - 1) / kWalk;
-    p.across = (p.vecs + kAcross - 1) / kAcross;
+    p.across = (unsigned)(((int64_t)p.vecs + kAcross - 1) / kAcross);
     if (((p.walks + p.seq.n) / kDown + 1) * p.across > INT32_MAX || (int64_t)p.seq.n * p.vecs / 128 >= INT32_MAX)
         return QSTATE_EUNSUPPORTED;
     if (dtype == QSTATE_BF16) {

@@ -299,3 +299,22 @@ def test_a_wait_that_runs_out_in_a_cut_scan(short_waits):
     M.debug_set()
     assert bool(torch.isnan(y).all()) and bool(torch.isnan(state).all()) and M.scan_timeouts() > before
     assert torch.equal(M.scan(x, dt, A, B, C, softplus=False), want)
+
+
+# ---------------------------------------------------------------- sizes at the end of their types
+@pytest.mark.parametrize("channels", [2 ** 31 - 1, 2 ** 31 - 31])
+def test_conv_of_the_most_channels(channels):
+    """One token of nearly 2^31 channels: as a prompt and as a step, the ends as those
+    of a narrow call."""
+    x, w = torch.zeros(1, channels, dtype=BF, device=DEV), torch.zeros(channels, 2, dtype=BF, device=DEV)
+    st = torch.zeros(1, 1, channels, dtype=BF, device=DEV)
+    g = gen(1)
+    for t in (x[0], st[0, 0]):
+        t[:99], t[-99:] = normal(g, 99), normal(g, 99)
+    w[:99], w[-99:] = normal(g, 99, 2), normal(g, 99, 2)
+    ends = lambda t: torch.cat([t[..., :99], t[..., -99:]], -1)  # noqa: E731
+    narrow = ends(st)
+    want = M.conv(ends(x), torch.cat([w[:99], w[-99:]]), state=narrow, initial=True)
+    kept = st.clone()
+    assert torch.equal(ends(M.conv(x, w, state=st, initial=True)), want) and torch.equal(ends(st), narrow)
+    assert torch.equal(ends(M.conv_step(x, w, state=kept)), want) and torch.equal(ends(kept), narrow)
