@@ -6,7 +6,10 @@ libqstate.so (csrc/) is the quantized recurrent-state step, libqmixer.so
 (csrc/mixer/) the operators around it, and _qmixer_usual.so (csrc/mixer/binding/) the
 module that makes their usual calls from Python.  Each .cu unit is compiled in parallel,
 then each library is linked with a static CUDA runtime; a library whose
-sources are older than it is left alone.  No fast-math: the step's arithmetic
+sources are older than it is left alone.  The two libraries need nvcc alone; the
+module needs PyTorch's headers and g++ too and is left out, with a message, where no
+PyTorch with CUDA is installed.  It is built for one version of PyTorch and of Python, whose
+numbers it holds: another one builds it anew.  No fast-math: the step's arithmetic
 is specified to the bit (see include/qstate.h), so FMA contraction is disabled
 and every fused multiply-add in the kernels is written explicitly.
 """
@@ -51,8 +54,30 @@ def _lib_up_to_date(lib) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps(lib))
 
 
+def usual_versions() -> str:
+    """What the module's binary interface goes by: the interpreter's and PyTorch's versions
+    ("" without a PyTorch that uses CUDA)."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return "" if torch.version.cuda is None else f"{sys.implementation.cache_tag} torch {torch.__version__}"
+
+
+def usual_built_for(versions: str) -> bool:
+    """Whether the module in the package was built for these versions."""
+    try:
+        with open(USUAL, "rb") as f:
+            return f"[built for {versions}]".encode() in f.read()
+    except FileNotFoundError:
+        return False
+
+
 def _usual_up_to_date() -> bool:
-    return os.path.exists(USUAL) and all(
+    versions = usual_versions()
+    if not versions:                 # nothing could load it
+        return True
+    return usual_built_for(versions) and all(
         os.path.getmtime(d) <= os.path.getmtime(USUAL)
         for d in (USUAL_SRC, os.path.join(ROOT, "include", "qmixer.h"), __file__))
 
@@ -64,10 +89,14 @@ def up_to_date() -> bool:
 def _build_usual():
     import sysconfig
 
+    versions = usual_versions()
+    if not versions:
+        print("no PyTorch with CUDA is installed: _qmixer_usual.so, which qmixer.py uses, is left out", file=sys.stderr)
+        return
     from torch.utils import cpp_extension
     tmp = USUAL + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-o", tmp, USUAL_SRC,
-           "-I" + os.path.join(ROOT, "include"), "-I" + sysconfig.get_paths()["include"],
+           f'-DBUILT_FOR="[built for {versions}]"', "-I" + os.path.join(ROOT, "include"), "-I" + sysconfig.get_paths()["include"],
            "-I/usr/local/cuda/include"]
     cmd += ["-isystem" + d for d in cpp_extension.include_paths()]
     cmd += [f for d in cpp_extension.library_paths() for f in ("-L" + d, "-Wl,-rpath," + d)]

@@ -329,7 +329,8 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(conv), ENTRY(conv_step), ENTRY(scan), ENTRY(scan_step), ENTRY(norm),
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmixer_usual", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// The versions of Python and PyTorch whose binary interface this is; build.py looks for it.
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmixer_usual", BUILT_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

@@ -57,6 +57,10 @@ class _Load:
         if not os.path.exists(build.USUAL):
             raise RuntimeError(f"{build.USUAL} is missing: build it with "
                                "`python -m bit_recurrent_state_decode_b200.build`")
+        if not build.usual_built_for(build.usual_versions()):
+            # of another binary interface: loading it could do anything
+            raise RuntimeError(f"{build.USUAL} was built for other versions of Python or PyTorch: build it again with "
+                               "`python -m bit_recurrent_state_decode_b200.build`")
         from . import _qmixer_usual
         _usual = _qmixer_usual
         return getattr(_usual, name)

@@ -38,3 +38,32 @@ def test_more_heads_than_a_grid_are_refused(M, heads, d_v):
                 C_stride=64, D=0, dt_bias=0, state=4096, y=4096, y_stride=row, seq_starts=0, sequences=1, tokens=8,
                 heads=heads, groups=1, d_k=64, d_v=d_v, dtype=1, dt_dtype=0, flags=4, workspace=4096,
                 workspace_bytes=2 ** 40) == U
+
+
+# ---------------------------------------------------------------- the build
+def child(code):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    return subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+
+
+def test_the_libraries_build_without_pytorch(M):
+    """A C user has nvcc alone: nothing of the build may need PyTorch but the module
+    that only Python loads."""
+    r = child("import sys; sys.modules['torch'] = None\n"
+              "from bit_recurrent_state_decode_b200 import build\n"
+              "print(build.build() == build.LIB, build.up_to_date())\n"
+              "build._build_usual()")
+    assert r.returncode == 0 and r.stdout.split() == ["True", "True"], r.stdout + r.stderr
+    assert "left out" in r.stderr
+
+
+def test_a_module_for_other_versions_is_built_again_and_not_loaded(M, monkeypatch):
+    from bit_recurrent_state_decode_b200 import build
+    assert build._usual_up_to_date() and build.usual_built_for(build.usual_versions())
+    monkeypatch.setattr(build, "usual_versions", lambda: "cpython-399 torch 99.0")
+    assert not build._usual_up_to_date() and not build.up_to_date()
+    with pytest.raises(RuntimeError, match="other versions"):
+        M._Load().norm
