@@ -22,9 +22,22 @@ namespace {
 
 using at::Tensor;
 
+// Whether two tensors' memory is apart, by their bounds.
+bool apart(const Tensor& a, const Tensor& b) {
+    auto span = [](const Tensor& t) {
+        int64_t n = 1;
+        for (int d = 0; d < t.dim(); d++) n += (t.size(d) - 1) * t.stride(d);
+        return n * (int64_t)t.element_size();
+    };
+    const char *pa = static_cast<const char*>(a.data_ptr()), *pb = static_cast<const char*>(b.data_ptr());
+    return pa >= pb + span(b) || pb >= pa + span(a);
+}
+
 struct Call {
     bool ok = true;
     int device = -1;
+    const Tensor* seen[16];          // the operands so far
+    int n_seen = 0;
 
     // a CUDA tensor of the current device that no gradient is wanted for and that
     // carries no forward-mode tangent
@@ -41,7 +54,15 @@ struct Call {
         } else if (t.get_device() != device) ok = false;
         if (ok && t.requires_grad() && c10::GradMode::is_enabled()) ok = false;
         if (ok && t._fw_grad(0).defined()) ok = false;
-        return ok ? &t : nullptr;
+        if (!ok) return nullptr;
+        seen[n_seen++] = &t;
+        return &t;
+    }
+    // whether the last operand, which the call writes, shares no memory with another
+    bool last_alone() const {
+        for (int i = 0; i + 1 < n_seen; i++)
+            if (!apart(*seen[n_seen - 1], *seen[i])) return false;
+        return true;
     }
     // nothing, or a contiguous vector of n
     const void* vector(PyObject* o, at::ScalarType type, int64_t n) {
@@ -81,17 +102,6 @@ int64_t rows(const Tensor& t, int inner) {
     }
     if (stride < 0) return row;
     return stride < row ? -1 : stride;
-}
-
-// Whether two tensors' memory is apart, by their bounds.
-bool apart(const Tensor& a, const Tensor& b) {
-    auto span = [](const Tensor& t) {
-        int64_t n = 1;
-        for (int d = 0; d < t.dim(); d++) n += (t.size(d) - 1) * t.stride(d);
-        return n * (int64_t)t.element_size();
-    };
-    const char *pa = static_cast<const char*>(a.data_ptr()), *pb = static_cast<const char*>(b.data_ptr());
-    return pa >= pb + span(b) || pb >= pa + span(a);
 }
 
 bool on16(const Tensor& t) { return (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0; }
@@ -171,7 +181,7 @@ PyObject* conv_any(PyObject* const* a, bool step) {
     if (!c.ok || p.sequences > INT32_MAX || p.tokens > INT32_MAX) return none();
     if (state && (state->scalar_type() != x->scalar_type() || state->dim() != 3 || state->size(0) != p.sequences ||
                   state->size(1) != width - 1 || state->size(2) != channels || !state->is_contiguous() ||
-                  !apart(*state, *x) || !apart(*state, *w)))
+                  !c.last_alone()))
         return none();
     Tensor y = at::empty(x->sizes(), x->options());
     const int32_t act = a[4] == Py_True ? QMIXER_SILU : 0;
@@ -219,7 +229,7 @@ PyObject* scan_any(PyObject* const* a, bool step) {
     if (!c.ok || p.sequences > INT32_MAX || p.tokens > INT32_MAX) return none();
     if (state && (state->scalar_type() != at::kFloat || state->dim() != 4 || state->size(0) != p.sequences ||
                   state->size(1) != heads || state->size(2) != d_k || state->size(3) != d_v || !state->is_contiguous() ||
-                  !apart(*state, *x) || !apart(*state, *dt) || !apart(*state, *B) || !apart(*state, *C)))
+                  !c.last_alone()))
         return none();
     const int32_t flags = (a[8] == Py_True ? QMIXER_SOFTPLUS : 0) | (initial ? QMIXER_INITIAL : 0);
     float* S = state ? static_cast<float*>(state->data_ptr()) : nullptr;
@@ -267,9 +277,7 @@ PyObject* norm_any(PyObject* const* a) {
         other = c.tensor(a[2]);
         if (!other || other->scalar_type() != x->scalar_type() || other->sizes() != x->sizes()) return none();
         os = rows(*other, 1);
-        if (os < 0 || (before == QMIXER_BEFORE_RESIDUAL &&
-                       (!apart(*other, *x) || !apart(*other, THPVariable_Unpack(a[1])))))
-            return none();
+        if (os < 0 || (before == QMIXER_BEFORE_RESIDUAL && !c.last_alone())) return none();
     }
     Tensor y = at::empty(x->sizes(), kind == QMIXER_OUT_INT8   ? x->options().dtype(at::kChar)
                                      : kind == QMIXER_OUT_E4M3 ? x->options().dtype(at::kFloat8_e4m3fn)

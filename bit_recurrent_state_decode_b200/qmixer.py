@@ -165,6 +165,8 @@ def _rows(fn, name, t, inner):
 
 
 def _span(t):
+    if t.is_contiguous():
+        return t.nbytes
     return (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size() if t.numel() else 0
 
 
@@ -241,11 +243,23 @@ def _fresh(like, dtype):
 
 
 def _given(fn, out, like, shape, dtype, inputs):
-    """The caller's `out`, apart from the inputs."""
+    """The caller's `out`, apart from the inputs {name: tensor or None}."""
     _tensor(fn, "out", out, like.get_device(), dtype, shape)
-    for name, t in inputs:
-        _apart(fn, "out", out, name, t)
+    _alone(fn, "out", out, inputs)
     return out
+
+
+def _alone(fn, name, a, inputs):
+    """_apart of each of the inputs {name: tensor or None}, by bounds first."""
+    if a is None:
+        return
+    at = a.data_ptr()
+    end = at + _span(a)
+    for other, b in inputs.items():
+        if b is not None:
+            first = b.data_ptr()
+            if first < end and at < first + _span(b):
+                _apart(fn, name, a, other, b)
 
 
 # ---------------------------------------------------------------- convolution
@@ -270,7 +284,8 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
         raise ValueError(f"{fn}: x must be [batch, length, channels] or [tokens, channels]")
     shape, index, code = x.shape, x.get_device(), _code(fn, x)
     n, tokens, starts = _sequences(fn, shape[:-1], seq_starts, index)
-    width, wp, bp, sp = _taps(fn, x, weight, bias, state, n, index)
+    inputs = {"x": x, "weight": weight, "bias": bias, "seq_starts": seq_starts}
+    width, wp, bp, sp = _taps(fn, x, weight, bias, state, n, index, inputs)
     if initial and state is None:
         raise ValueError(f"{fn}: initial=True needs the state to continue from")
     xs = _rows(fn, "x", x, 1)
@@ -279,7 +294,7 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
         if out is None:
             y, ys = _fresh(x, x.dtype), shape[-1]
         else:
-            y = _given(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
+            y = _given(fn, out, x, shape, x.dtype, {**inputs, "state": state})
             ys = _rows(fn, "out", y, 1)
         _conv(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), ys, starts, n, tokens, shape[-1],
               width, code, (INITIAL if initial else 0) | (SILU if activation else 0))
@@ -301,14 +316,15 @@ def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=
     if state is None:
         raise ValueError(f"{fn}: state is required")
     shape, code = x.shape, _code(fn, x)
-    width, wp, bp, sp = _taps(fn, x, weight, bias, state, shape[0], x.get_device())
+    inputs = {"x": x, "weight": weight, "bias": bias}
+    width, wp, bp, sp = _taps(fn, x, weight, bias, state, shape[0], x.get_device(), inputs)
     xs = _rows(fn, "x", x, 1)
 
     def body(st):
         if out is None:
             y, ys = _fresh(x, x.dtype), shape[1]
         else:
-            y = _given(fn, out, x, shape, x.dtype, (("x", x), ("state", state), ("weight", weight), ("bias", bias)))
+            y = _given(fn, out, x, shape, x.dtype, {**inputs, "state": state})
             ys = _rows(fn, "out", y, 1)
         _conv_step(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), ys, shape[0], shape[1], width,
                    code, SILU if activation else 0)
@@ -316,7 +332,7 @@ def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=
     return _launch(fn, x, stream, body)
 
 
-def _taps(fn, x, weight, bias, state, n, index):
+def _taps(fn, x, weight, bias, state, n, index, inputs):
     channels, dtype = x.shape[-1], x.dtype
     _tensor(fn, "weight", weight, index, dtype)
     if weight.dim() != 2 or weight.shape[0] != channels or not weight.is_contiguous():
@@ -326,9 +342,7 @@ def _taps(fn, x, weight, bias, state, n, index):
     sp = 0
     if state is not None:
         sp = _dense(fn, "state", state, index, dtype, (n, width - 1, channels))
-        at = x.data_ptr()       # by bounds first
-        if at < sp + state.nbytes and sp < at + x.shape[0] * max(x.stride(0), channels) * 4:
-            _apart(fn, "state", state, "x", x)
+        _alone(fn, "state", state, inputs)
     return width, weight.data_ptr(), bp, sp
 
 
@@ -380,15 +394,6 @@ def _workspace(index, *sizes):
     return size
 
 
-def _states_apart(fn, state, sp, rows, x, dt, B, C):
-    """_apart of the states and the inputs, by bounds first."""
-    end, reach = sp + state.nbytes, x.shape[:-2].numel() * 4
-    for i, name, t in ((0, "x", x), (2, "dt", dt), (5, "B", B), (7, "C", C)):
-        at = rows[i]
-        if at < end and sp < at + reach * rows[i + 1]:
-            _apart(fn, "state", state, name, t)
-
-
 def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, initial=False, seq_starts=None,
          out=None, stream=None):
     """Selective scan of a prompt: S <- exp(dt A) S + dt B x^T, y = S^T C + D x.
@@ -415,16 +420,17 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
     if initial and state is None:
         raise ValueError(f"{fn}: initial=True needs the state to continue from")
     heads, groups, d_k, d_v = sizes[:4]
+    inputs = {"x": x, "dt": dt, "A": A, "B": B, "C": C, "D": D, "dt_bias": dt_bias, "seq_starts": seq_starts}
     sp = 0
     if state is not None:
         sp = _dense(fn, "state", state, index, _F32, (n, heads, d_k, d_v))
-        _states_apart(fn, state, sp, rows, x, dt, B, C)
+        _alone(fn, "state", state, inputs)
 
     def body(st):
         if out is None:
             y, ys = _fresh(x, x.dtype), sizes[0] * sizes[3]
         else:
-            y = _given(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
+            y = _given(fn, out, x, x.shape, x.dtype, {**inputs, "state": state})
             ys = _rows(fn, "out", y, 2)
         size = _workspace(index, n, tokens, *sizes[:5])
         work = x.new_empty(size, dtype=torch.uint8) if size else None
@@ -468,13 +474,14 @@ def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out
     shape = x.shape
     n = shape[0]
     sp = _dense(fn, "state", state, index, _F32, (n, sizes[0], sizes[2], sizes[3]))
-    _states_apart(fn, state, sp, rows, x, dt, B, C)
+    inputs = {"x": x, "dt": dt, "A": A, "B": B, "C": C, "D": D, "dt_bias": dt_bias}
+    _alone(fn, "state", state, inputs)
 
     def body(st):
         if out is None:
             y, ys = _fresh(x, x.dtype), sizes[0] * sizes[3]
         else:
-            y = _given(fn, out, x, shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt), ("state", state)))
+            y = _given(fn, out, x, shape, x.dtype, {**inputs, "state": state})
             ys = _rows(fn, "out", y, 2)
         _scan_step(st, *rows, dp, biasp, sp, y.data_ptr(), ys, n, *sizes,
                    SOFTPLUS if softplus else 0)
@@ -541,7 +548,8 @@ def step(obj, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, out=None, 
         if out is None:
             y, ys = _fresh(x, x.dtype), sizes[0] * sizes[3]
         else:
-            y = _given(fn, out, x, x.shape, x.dtype, (("x", x), ("B", B), ("C", C), ("dt", dt)))
+            y = _given(fn, out, x, x.shape, x.dtype,
+                       {"x": x, "dt": dt, "A": A, "B": B, "C": C, "D": D, "dt_bias": dt_bias})
             ys = _rows(fn, "out", y, 2)
         if n == 0:
             return y
@@ -600,18 +608,14 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
         o2 = _flat(fn, name, other)
         op, ostride = o2.data_ptr(), _rows(fn, name, o2, 1)
         if before == BEFORE_RESIDUAL:
-            at, reach = x2.data_ptr(), x2.shape[0] * 4                   # by bounds first
-            if at < op + o2.shape[0] * ostride * 4 and op < at + reach * xs:
-                _apart(fn, name, o2, "x", x2)
-            if wp < op + o2.shape[0] * ostride * 4 and op < wp + weight.nbytes:
-                _apart(fn, name, o2, "weight", weight)
+            _alone(fn, name, o2, {"x": x2, "weight": weight})
 
     def body(st):
         if out is None:
             y = y2 = _fresh(x, dtype or xd)
             ys = columns
         else:
-            y = _given(fn, out, x, shape, dtype or xd, (("x", x), (name, other), ("weight", weight)))
+            y = _given(fn, out, x, shape, dtype or xd, {"x": x, name: other, "weight": weight})
             y2 = _flat(fn, "out", y)
             ys = _rows(fn, "out", y2, 1)
         scale, sp = scales, 0
@@ -621,8 +625,7 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
                 scale = x.new_empty(want, dtype=_F32)
             else:
                 _dense(fn, "scales", scale, index, _F32, want)
-                for other_name, t in (("x", x2), (name, other), ("weight", weight), ("out", y2)):
-                    _apart(fn, "scales", scale, other_name, t)
+                _alone(fn, "scales", scale, {"x": x2, name: other, "weight": weight, "out": y2})
             sp = scale.data_ptr()
         _norm(st, x2.data_ptr(), xs, op, ostride, wp, y2.data_ptr(), ys, sp, x2.shape[0],
               columns, group, eps, code, before, kind)

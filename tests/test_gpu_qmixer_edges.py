@@ -318,3 +318,54 @@ def test_conv_of_the_most_channels(channels):
     kept = st.clone()
     assert torch.equal(ends(M.conv(x, w, state=st, initial=True)), want) and torch.equal(ends(st), narrow)
     assert torch.equal(ends(M.conv_step(x, w, state=kept)), want) and torch.equal(ends(kept), narrow)
+
+
+def overlapping(name):
+    """(written operand, the other, a call with the two in one piece of memory): every
+    pair of what an operator writes and what it reads."""
+    fn, tensors, kw = operands()[name]
+    tensors = {n: t.to(F) for n, t in tensors.items()}
+    starts = {}
+    if name in ("conv", "scan"):
+        starts = dict(seq_starts=torch.tensor([0, 4], dtype=torch.int32, device=DEV))
+    written = [n for n in ("state", "residual") if n in tensors]
+    if "step" != name and name != "load":
+        like = tensors["x"]
+        tensors = {**tensors, "out": torch.empty_like(like)}
+        written.append("out")
+    elif name == "step":
+        tensors = {**tensors, "out": torch.empty_like(tensors["x"])}
+        written.append("out")
+    for w in written:
+        for other, t in {**tensors, **starts}.items():
+            if other == w or (other == "out" and w != "out"):
+                continue
+            both = torch.zeros(tensors[w].numel() + t.numel(), device=DEV)
+            args = {k: v for k, v in tensors.items() if k != "out" or "out" in (w, other)}
+            shared = both[:tensors[w].numel()].view(tensors[w].shape)
+            # (the other one starts with the last 16 bytes of the written one)
+            begin = tensors[w].numel() - 4
+            inside = both[begin:begin + t.numel()].view(t.dtype).view(t.shape)
+            yield w, other, lambda args=args, w=w, other=other, shared=shared, inside=inside: fn(
+                **{**args, **starts, w: shared, other: inside}, **kw)
+
+
+@pytest.mark.parametrize("name", ["conv", "conv_step", "scan", "scan_step", "norm", "norm gated", "step"])
+def test_what_is_written_is_apart_from_what_is_read(name):
+    seen = 0
+    for w, other, call in overlapping(name):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+        seen += 1
+    assert seen >= 2
+
+
+def test_a_view_of_one_sequence_is_taken_as_far_as_it_reaches():
+    """x of one sequence whose leading stride says nothing about its length."""
+    both = torch.zeros(40 * 64 + 3 * 64, device=DEV)
+    x = both.as_strided((1, 40, 64), (0, 64, 1))
+    w = torch.ones(64, 4, device=DEV)
+    M.conv(x, w, state=both[40 * 64:].view(1, 3, 64))
+    for out in (None, torch.empty(1, 40, 64, device=DEV)):
+        with pytest.raises(ValueError, match="state overlaps x"):
+            M.conv(x, w, state=both[20 * 64:23 * 64].view(1, 3, 64), out=out)
