@@ -104,6 +104,12 @@ int64_t rows(const Tensor& t, int inner) {
     return stride < row ? -1 : stride;
 }
 
+// What a call has written in place, autograd learns by its version: an operation that
+// saved the former values for its backward pass must not go on with these.
+void written(const Tensor* t) {
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 bool on16(const Tensor& t) { return (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0; }
 
 PyObject* none() { Py_RETURN_NONE; }
@@ -120,9 +126,11 @@ bool taken(const char* entry, int rc) {
     if (rc == QSTATE_EINVAL || rc == QSTATE_EUNSUPPORTED) return false;
     throw Launched{entry, rc};
 }
-// The outputs of a call that was taken, as Python objects (one, or a pair).
-PyObject* wrapped(const char* entry, Tensor& y, Tensor* scales = nullptr) {
+// The outputs of a call that was taken, as Python objects (one, or a pair); `in_place`:
+// what else it wrote, or NULL.
+PyObject* wrapped(const char* entry, const Tensor* in_place, Tensor& y, Tensor* scales = nullptr) {
     try {
+        written(in_place);
         PyObject* first = THPVariable_Wrap(std::move(y));
         if (!scales) return first;
         PyObject *second = THPVariable_Wrap(std::move(*scales)), *both = nullptr;
@@ -197,7 +205,7 @@ PyObject* conv_any(PyObject* const* a, bool step) {
                                  (int32_t)width, type, act | (initial ? QMIXER_INITIAL : 0)};
         rc = qmixer_conv(&q, c.stream());
     }
-    return taken(entry, rc) ? wrapped(entry, y) : none();
+    return taken(entry, rc) ? wrapped(entry, state, y) : none();
 }
 
 // ---------------------------------------------------------------- selective scan
@@ -239,7 +247,7 @@ PyObject* scan_any(PyObject* const* a, bool step) {
                                       bias, S, y.data_ptr(), heads * d_v, (int32_t)x->size(0), (int32_t)heads,
                                       (int32_t)groups, (int32_t)d_k, (int32_t)d_v, type, dt_type, flags};
         const char* const entry = "qmixer_scan_step";
-        return taken(entry, qmixer_scan_step(&q, c.stream())) ? wrapped(entry, y) : none();
+        return taken(entry, qmixer_scan_step(&q, c.stream())) ? wrapped(entry, state, y) : none();
     }
     const int64_t bytes = qmixer_scan_workspace((int32_t)p.sequences, p.tokens, (int32_t)heads, (int32_t)groups,
                                                 (int32_t)d_k, (int32_t)d_v, type);
@@ -251,7 +259,7 @@ PyObject* scan_any(PyObject* const* a, bool step) {
                              (int32_t)groups, (int32_t)d_k, (int32_t)d_v, type, dt_type, flags,
                              bytes ? work.data_ptr() : nullptr, bytes};
     const char* const entry = "qmixer_scan";
-    return taken(entry, qmixer_scan(&q, c.stream())) ? wrapped(entry, y) : none();
+    return taken(entry, qmixer_scan(&q, c.stream())) ? wrapped(entry, state, y) : none();
 }
 
 // ---------------------------------------------------------------- norm
@@ -293,7 +301,7 @@ PyObject* norm_any(PyObject* const* a) {
                              (int32_t)columns, (int32_t)group, (float)eps, type, (int32_t)before, (int32_t)kind};
     const char* const entry = "qmixer_norm";
     if (!taken(entry, qmixer_norm(&q, c.stream()))) return none();
-    return wrapped(entry, y, kind ? &scales : nullptr);
+    return wrapped(entry, before == QMIXER_BEFORE_RESIDUAL ? other : nullptr, y, kind ? &scales : nullptr);
 }
 
 // ---------------------------------------------------------------- module

@@ -249,6 +249,14 @@ def _given(fn, out, like, shape, dtype, inputs):
     return out
 
 
+def _written(*tensors):
+    """What a call has written in place, autograd learns by its version: an operation that
+    saved the former values for its backward pass must not go on with these."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _alone(fn, name, a, inputs):
     """_apart of each of the inputs {name: tensor or None}, by bounds first."""
     if a is None:
@@ -298,6 +306,7 @@ def conv(x, weight, bias=None, *, state=None, initial=False, seq_starts=None, ac
             ys = _rows(fn, "out", y, 1)
         _conv(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), ys, starts, n, tokens, shape[-1],
               width, code, (INITIAL if initial else 0) | (SILU if activation else 0))
+        _written(state, out)
         return y
     return _launch(fn, x, stream, body)
 
@@ -328,6 +337,7 @@ def conv_step(x, weight, bias=None, *, state, activation=True, out=None, stream=
             ys = _rows(fn, "out", y, 1)
         _conv_step(st, x.data_ptr(), xs, wp, bp, sp, y.data_ptr(), ys, shape[0], shape[1], width,
                    code, SILU if activation else 0)
+        _written(state, out)
         return y
     return _launch(fn, x, stream, body)
 
@@ -436,6 +446,7 @@ def scan(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state=None, ini
         work = x.new_empty(size, dtype=torch.uint8) if size else None
         _scan(st, *rows, dp, biasp, sp, y.data_ptr(), ys, starts, n, tokens, *sizes,
               (INITIAL if initial else 0) | (SOFTPLUS if softplus else 0), work.data_ptr() if size else 0, size)
+        _written(state, out)
         return y
     return _launch(fn, x, stream, body)
 
@@ -485,6 +496,7 @@ def scan_step(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, state, out
             ys = _rows(fn, "out", y, 2)
         _scan_step(st, *rows, dp, biasp, sp, y.data_ptr(), ys, n, *sizes,
                    SOFTPLUS if softplus else 0)
+        _written(state, out)
         return y
     return _launch(fn, x, stream, body)
 
@@ -559,6 +571,7 @@ def step(obj, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, out=None, 
         obj.step(q, k, v, gates, o, torch.cuda.current_stream())
         _step_output(st, o.data_ptr(), rows[0], rows[1], dp, y.data_ptr(), ys, n, sizes[0],
                      sizes[3], sizes[4])
+        _written(out)
         return y
     return _launch(fn, x, stream, body)
 
@@ -629,6 +642,7 @@ def norm(x, weight, *, residual=None, gate=None, eps=1e-5, dtype=None, group=0, 
             sp = scale.data_ptr()
         _norm(st, x2.data_ptr(), xs, op, ostride, wp, y2.data_ptr(), ys, sp, x2.shape[0],
               columns, group, eps, code, before, kind)
+        _written(residual, out, scales)
         return (y, scale) if kind else y
     return _launch(fn, x, stream, body)
 

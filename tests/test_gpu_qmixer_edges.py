@@ -369,3 +369,34 @@ def test_a_view_of_one_sequence_is_taken_as_far_as_it_reaches():
     for out in (None, torch.empty(1, 40, 64, device=DEV)):
         with pytest.raises(ValueError, match="state overlaps x"):
             M.conv(x, w, state=both[20 * 64:23 * 64].view(1, 3, 64), out=out)
+
+
+# ---------------------------------------------------------------- autograd beside the calls
+@pytest.mark.parametrize("name", ["conv", "conv_step", "scan", "scan_step", "norm", "step"])
+@pytest.mark.parametrize("given", [False, True])
+def test_what_is_written_in_place_is_known_to_autograd(name, given):
+    """A product that saved a state or residual for its backward pass is not given the
+    values behind the call in their place; inference tensors have no versions."""
+    fn, tensors, kw = operands()[name]
+    if given:
+        tensors["out"] = torch.empty_like(tensors["x"])
+    written = [n for n in ("state", "residual", "out") if n in tensors]
+    for n in written:
+        w = torch.ones_like(tensors[n], requires_grad=True)
+        p = (tensors[n] * w).sum()
+        fn(**tensors, **kw)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            p.backward()
+    for t in (t for n, t in tensors.items() if n not in written):
+        assert t._version == 0
+    with torch.inference_mode():
+        tensors = {n: t.clone() for n, t in tensors.items()}
+    fn(**tensors, **kw)
+
+
+def test_norm_scales_of_the_caller_are_known_to_autograd():
+    x, w = normal(gen(1), 4, 64), torch.ones(64, device=DEV)
+    scales = torch.ones(4, 1, device=DEV)
+    v = scales._version
+    M.norm(x, w, dtype=torch.int8, scales=scales)
+    assert scales._version == v + 1
