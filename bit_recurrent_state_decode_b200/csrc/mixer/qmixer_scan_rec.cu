@@ -17,13 +17,17 @@
 // of y over 128 rows, stays below 2^13 2^65 2^7 2^40 = 2^125.  From the first token on
 // whose c leaves its range the batch takes the plain form, from the first that breaks
 // another of these bounds on all of the segment: whatever a later token holds, an
-// earlier one is computed alike.  A token then costs 32 packed instructions and five
-// 16-byte shared loads a thread: instruction issue is the bound, not memory.  kBatch tokens are staged at a time while the next ones are on
-// their way to registers.  The 8 or 16 threads of a column leave their parts of y in
-// shared memory, where they are added once per batch (shuffles within the token
-// took a fifth of the instructions and most of the waiting).  Eight sequences of 1024
-// tokens, 32 heads of 128 x 64, take 344 us (367 with the decay in every token); the
-// packed instructions alone would take 120, issuing every other cycle.
+// earlier one is computed alike.
+//
+// A token then costs 32 packed instructions and five 16-byte shared loads a thread.
+// kBatch tokens are staged at a time while the next ones are on their way to registers.
+// The 8 or 16 threads of a column leave their parts of y in shared memory, where they
+// are added once per batch (shuffles within the token took a fifth of the instructions
+// and most of the waiting).  Eight sequences of 1024 tokens, 32 heads of 128 x 64, take
+// 344 us (367 with the decay in every token, 333 without the range's checks).  No pipe
+// bounds it: the multipliers are busy for 49% of the time and 43% of the issue slots are
+// used; 13 of 64 warps are there, which wait for shared loads, the two barriers of a
+// batch and one another's results, a warp 1.8, 1.5 and 1.4 times as long as it issues.
 #include <type_traits>
 
 #include "qmixer_scan.cuh"

@@ -67,3 +67,28 @@ def test_a_module_for_other_versions_is_built_again_and_not_loaded(M, monkeypatc
     assert not build._usual_up_to_date() and not build.up_to_date()
     with pytest.raises(RuntimeError, match="other versions"):
         M._Load().norm
+
+
+# ---------------------------------------------------------------- the plan of a cut prompt
+@pytest.mark.parametrize("sequences,tokens,H,N,P,dtype,ragged,segments", [
+    (1, 16001, 16, 128, 128, 1, False, 9),           # nine of 1792 tokens
+    (7, 3001, 16, 64, 64, 0, True, 3001 // 64 + 7),  # of 64 tokens, and room for each sequence's last
+    (8, 16384, 32, 128, 64, 1, False, 0),            # uncut
+    (8, 8192, 32, 128, 64, 0, False, 0),
+])
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the last call would launch")
+def test_plan_of_the_documented_sizes(M, sequences, tokens, H, N, P, dtype, ragged, segments):
+    """The least workspace that a call takes is that of the segments which the comments
+    and tables name (148 SMs)."""
+    need = segments * H * N * P * 4 + (segments * H * 4 + 15) // 16 * 16
+    starts = 4096 if ragged else 0
+
+    def rc(size):
+        return call(M, "qmixer_scan", x=4096, x_stride=H * P, dt=4096, dt_stride=H, A=4096, B=4096, B_stride=N, C=4096,
+                    C_stride=N, D=0, dt_bias=0, state=0, y=4096, y_stride=H * P, seq_starts=starts, sequences=sequences,
+                    tokens=tokens, heads=H, groups=1, d_k=N, d_v=P, dtype=dtype, dt_dtype=0, flags=4, workspace=4096,
+                    workspace_bytes=size)
+    assert M.lib().qmixer_scan_workspace(sequences, tokens, H, 1, N, P, dtype) >= need
+    assert rc(need) == -3                            # as far as the launch, for which there is no GPU
+    if need:
+        assert rc(need - 1) == E
