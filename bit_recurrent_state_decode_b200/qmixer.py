@@ -7,14 +7,19 @@ operators around the recurrent state of a Mamba2 layer.
     step                 the selective step of one token on a ``qstate.QState``
     norm                 root-mean-square norm, with a residual or a gate, and 8-bit output
 
+    scan_timeouts        blocks of prompt scans that gave up a bounded wait
+
 Argument checks and marshalling only: the arithmetic runs in the CUDA kernels
 of the library.  A usual call (its own output, the current stream) is checked and
-launched by the compiled module _qmixer_usual; what that leaves takes the way below.  Calls are asynchronous on the current stream of the tensors'
-device, or on `stream`; tensors of another stream have to be ordered before
-the call by the caller, as for any PyTorch operator.  The library must have
-been built; there is no CPU fallback and no autograd: inputs that require a
-gradient are refused while gradients are recorded, inputs with a forward-mode
-tangent always.
+launched by the compiled module _qmixer_usual; what that leaves takes the way below.
+Calls are asynchronous on the current stream of the tensors' device, or on
+`stream`, to which an output made by the call then belongs; tensors of another
+stream have to be ordered before the call by the caller and kept until it has run
+(Tensor.record_stream), as for any PyTorch operator.  What is written may not share
+memory with what is read.  The library must have been built; there is no CPU fallback
+and no autograd: inputs that require a gradient are refused while gradients are
+recorded, inputs with a forward-mode tangent always, and what a call writes in place
+counts as a new version of the tensor.
 """
 from __future__ import annotations
 

@@ -19,9 +19,18 @@
  *              with QMIXER_SILU, else z   (bias may be NULL: 0)
  *   norm       h = x + residual, x silu(gate) or x;
  *              y = h / sqrt(mean(h^2) + eps) * weight
- * The prompt scan of bfloat16 inputs forms its matrix products on the tensor
- * cores with binary32 sums; csrc/mixer/qmixer_scan_chunk.cu says which
- * factors it rounds to bfloat16 there.
+ * The prompt scan of bfloat16 inputs forms its matrix products over chunks of
+ * 128 tokens on the tensor cores, with binary32 sums.  Its states keep 24 bits.
+ * For y alone it rounds two factors to bfloat16: (C B^T) decays dt, and the copy
+ * of S that C multiplies.  Each is off by at most 2^-8 of a term of y, so y by
+ * 2^-7 of the sum of its terms' magnitudes, beside its own rounding: 0.0018 to
+ * 0.0020 in the 2-norm where the rounding of y alone gives 0.0017.  C B^T, dt x
+ * and the products of up to 128 decays are formed by themselves there, and in
+ * either form of a long prompt the products of a whole segment's decays: these
+ * have to stay inside binary32 (products of decays of at most 1 do).  In the
+ * form for bfloat16 a token whose x is not a finite number makes its column of y
+ * and of the state NaN from its own row on, where the binary32 form may keep an
+ * infinity; no other column and no earlier token depends on it in either.
  *
  * SEQUENCES.  The token axis of the prompt calls holds `sequences` sequences
  * one behind the other.  seq_starts (device, int32 [sequences + 1], ascending,
@@ -220,10 +229,11 @@ int qmixer_step_output(const qmixer_step_output_args* args, qstate_stream stream
  * of each `group` consecutive columns (a power of two from 8 to 256 dividing
  * columns).  scale = max|y| / Qmax, Qmax 127 (int8) or 448 (e4m3), code = y /
  * scale, both quotients rounded to binary32 first, the code then half to even
- * (int8) or to nearest even (e4m3), and clamped to Qmax.  y's own binary32
- * value is within a few units: its root and silu are the hardware's to 2
- * units.  Where max|y| is 0 the scale and codes are 0, where it is not a
- * finite number the scale is NaN and the codes 0.  columns 1 to 32768. */
+ * (int8) or to nearest even (e4m3), and clamped to Qmax.  (y's own binary32
+ * value is not the rounded one: the reciprocal root is off by up to 2 units, the
+ * silu of bfloat16 inputs by up to 10 + 2.4 |gate| of 2^-24.)  Where max|y| is 0
+ * the scale and codes are 0, where it is not a finite number the scale is NaN
+ * and the codes 0.  columns 1 to 32768. */
 typedef struct qmixer_norm_args {
     const void* x;
     int64_t x_stride;
